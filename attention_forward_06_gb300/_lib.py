@@ -33,11 +33,14 @@ SIGNATURES = {
         "attn_fwd_block_mask_words": (ctypes.c_size_t, [_c_int] * 4),
         "attn_fwd_ordered": (_c_int, [_vp, _vp, _vp, _vp, _vp] + [_c_int] * 7 + [_c_float, _vp, _c_int, _vp]),
         "attn_fwd_tile_order_entries": (ctypes.c_size_t, [_c_int] * 4),
+        "attn_fwd_window": (_c_int, [_vp, _vp, _vp, _vp, _vp] + [_c_int] * 9 + [_c_float, _vp]),
     },
     "attn_fwd_trace": {},  # filled below: attn_fwd's entry points and the trace reader
     "attn_bwd": {
         "attn_bwd": (_c_int, [_vp] * 9 + [_c_int] * 7 + [_c_float, _vp, ctypes.c_size_t, _vp]),
         "attn_bwd_workspace_size": (ctypes.c_size_t, [_c_int] * 3),
+        "attn_bwd_window": (_c_int, [_vp] * 9 + [_c_int] * 9 + [_c_float, _vp, ctypes.c_size_t, _vp]),
+        "attn_bwd_window_workspace_size": (ctypes.c_size_t, [_c_int] * 8),
         "attn_bwd_strerror": (ctypes.c_char_p, [_c_int]),
         "attn_bwd_debug_status": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
     },

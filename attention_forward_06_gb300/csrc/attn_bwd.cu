@@ -28,6 +28,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -84,6 +85,16 @@ struct BParams {
   int n_items;
   float c;      // scale * log2(e)
   float scale;
+  // window mode: key j also needs row + diag - j < window or j < sinks.  A key tile that
+  // holds sinks is seen by every later query tile; its dK/dV work is cut into sink_chunks
+  // items of sink_per query tiles, which leave fp32 partials (sink_chunks > 1) for
+  // attn_bwd_sink_kernel
+  int window;       // 1 .. max(Sq, Sk)
+  int sinks;        // 0 .. Sk
+  int sink_tiles;   // key tiles that hold sinks
+  int sink_chunks;  // items per such tile and kv slice
+  int sink_per;     // query tiles per chunk
+  float* sink_part; // [sink_tiles][sink_chunks][B*Hkv][dV, dK][BT][D]
 };
 
 __device__ int g_bwd_status;
@@ -241,6 +252,43 @@ __device__ __forceinline__ int first_qtile(const BParams& p, int j) {
   return first_row / BT;
 }
 
+// A dK/dV work item: key tile j of kv slice z against query tiles [i0, i0 + nI) of every
+// query head of the group.
+struct KvItem {
+  int j, z, i0, nI;
+  int part;  // window mode: the slot of the fp32 partial it writes (-1: it writes dK and dV)
+};
+
+template <bool WINDOW>
+__device__ __forceinline__ KvItem kv_item(const BParams& p, int x) {
+  KvItem it;
+  it.part = -1;
+  if constexpr (WINDOW) {
+    // the chunks of the tiles that hold sinks come first, then the other tiles in order
+    const int n_chunked = p.sink_tiles * p.sink_chunks;
+    const int y = x / p.BZ;
+    it.z = x % p.BZ;
+    if (y < n_chunked) {
+      it.j = y / p.sink_chunks;
+      it.i0 = first_qtile(p, it.j) + (y % p.sink_chunks) * p.sink_per;
+      it.nI = min(p.n_qt - it.i0, p.sink_per);
+      if (p.sink_chunks > 1) it.part = x;
+    } else {
+      it.j = y - n_chunked + p.sink_tiles;
+      it.i0 = first_qtile(p, it.j);
+      // the last row that has a key of the tile in its window
+      const int last = min(p.Sq, min(it.j * BT + BT, p.Sk) + p.window - 1 - p.diag) - 1;
+      it.nI = last < 0 ? 0 : last / BT + 1 - it.i0;
+    }
+  } else {
+    it.j = x / p.BZ;
+    it.z = x % p.BZ;
+    it.i0 = first_qtile(p, it.j);
+    it.nI = p.n_qt - it.i0;
+  }
+  return it;
+}
+
 // ---------------------------------------------------------------------------- dK, dV
 // Work item x: key tile j = x / (B*Hkv) (ascending: under a causal mask the
 // heaviest first), kv slice z = x % (B*Hkv).  A step is one 128-row query tile of
@@ -251,7 +299,9 @@ __device__ __forceinline__ int first_qtile(const BParams& p, int j) {
 // over the whole item.  Compute warpgroup r owns half r, so one half's
 // exponentials run while the tensor cores work on the other half:
 //   S_0(s) S_1(s) | dVdK_0(s) S_0(s+1) dVdK_1(s) S_1(s+1) | ...
-template <int D>
+// Window mode: the items of kv_item; a key tile without sinks meets only the query
+// tiles whose windows reach it.
+template <int D, bool WINDOW = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -266,7 +316,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain;
   __shared__ uint32_t tmem_slot, abort_flag;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int nz = p.BZ;
 
   if (threadIdx.x == 0) {
     mbar_init(&kv_full, 1);
@@ -311,9 +360,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k * static_cast<int>(gridDim.x) < p.n_items && ok; ++k) {
       const int x = item_of(k);
       if (x >= p.n_items) continue;
-      const int j = x / nz, z = x % nz;
-      const int i0 = first_qtile(p, j);
-      const int nI = p.n_qt - i0;
+      const KvItem item = kv_item<WINDOW>(p, x);
+      const int j = item.j, z = item.z, i0 = item.i0, nI = item.nI;
       if (nI <= 0) continue;
       if (n_ne > 0) ok = warp_wait(&kv_empty, (n_ne - 1) & 1, abort_v, kTimeoutNs);
       if (!ok) break;
@@ -385,8 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k * static_cast<int>(gridDim.x) < p.n_items && ok; ++k) {
       const int x = item_of(k);
       if (x >= p.n_items) continue;
-      const int j = x / nz;
-      const int nI = p.n_qt - first_qtile(p, j);
+      const int nI = kv_item<WINDOW>(p, x).nI;
       if (nI <= 0) continue;
       const int T = G * nI;  // steps of the item
       ok = warp_wait(&kv_full, n_ne & 1, abort_v, kTimeoutNs);
@@ -449,15 +496,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k * static_cast<int>(gridDim.x) < p.n_items && ok; ++k) {
       const int x = item_of(k);
       if (x >= p.n_items) continue;
-      const int j = x / nz;
-      const int i0 = first_qtile(p, j);
-      const int nI = p.n_qt - i0;
+      const KvItem item = kv_item<WINDOW>(p, x);
+      const int j = item.j, i0 = item.i0, nI = item.nI;
       const int key = j * BT + kk;
       const bool key_live = key < p.Sk;
       // this key's dV (warpgroup 0) or dK (warpgroup 1) row
-      auto grad_row = [&]() { return (r == 0 ? p.dv : p.dk) + (static_cast<int64_t>(x % nz) * p.Sk + key) * D; };
+      auto grad_row = [&]() { return (r == 0 ? p.dv : p.dk) + (static_cast<int64_t>(item.z) * p.Sk + key) * D; };
+      // this warp's rows of the item's fp32 partial dV or dK (window mode)
+      auto part_rows = [&]() {
+        return p.sink_part + ((static_cast<int64_t>(item.part) * 2 + r) * BT + quarter * 32) * D;
+      };
       if (nI <= 0) {  // no query row sees this key tile: zero gradients
-        if (key_live) {
+        if (WINDOW && item.part >= 0) {
+          float4* a4 = reinterpret_cast<float4*>(part_rows() + lane * D);
+#pragma unroll
+          for (int v4 = 0; v4 < D / 4; ++v4) a4[v4] = make_float4(0.f, 0.f, 0.f, 0.f);
+        } else if (key_live) {
           uint4* a4 = reinterpret_cast<uint4*>(grad_row());
 #pragma unroll
           for (int v4 = 0; v4 < D / 8; ++v4) a4[v4] = make_uint4(0u, 0u, 0u, 0u);
@@ -484,6 +538,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int first_ok = key_live ? (diag_tile ? key - p.diag - i * BT - BH2 * r : 0) : BH2;
 #pragma unroll
           for (int e = 0; e < 64; ++e) sv[e] = e >= first_ok ? sv[e] : __float_as_uint(-INFINITY);
+        }
+        if constexpr (WINDOW) {
+          // the tile's first key has left the window of some row: rows whose window is past this key
+          if (i * BT + BT - 1 + p.diag - j * BT >= p.window) {
+            const int end_ok = key < p.sinks ? BH2 : key + p.window - p.diag - i * BT - BH2 * r;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) sv[e] = e < end_ok ? sv[e] : __float_as_uint(-INFINITY);
+          }
         }
         // P = exp2(S c - LSE log2 e) and dS = P (dP - D), two rows per packed operation
         const uint64_t c2 = f2_pack(p.c, p.c);
@@ -523,6 +585,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n_ne;
       tc_fence_after();
       const float mul = r == 0 ? 1.0f : p.scale;
+      if (WINDOW && item.part >= 0) {  // fp32 partial rows, 128 bytes (32 columns) at a time
+        uint8_t* pbase = reinterpret_cast<uint8_t*>(part_rows());
+#pragma unroll
+        for (int cb = 0; cb < D / 32; ++cb) {
+          uint32_t a[32];
+          tmem_ld32_wait(acc_t + 32 * cb, a);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(__uint_as_float(a[e]) * mul);
+          store_warp_rows<8>(a, pbase + 128 * cb, 4 * D, 32, lane);
+        }
+        tc_fence_before();
+        mbar_arrive(&acc_empty);
+        ATTN_TR(24, x);
+        continue;
+      }
       // the warp's 32 keys' rows, 64 bytes (32 columns) at a time
       uint8_t* wbase = reinterpret_cast<uint8_t*>(grad_row() - lane * D);
       const int live_keys = p.Sk - (j * BT + quarter * 32);
@@ -551,12 +628,60 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Window mode: dV and dK of the key tiles that hold sinks, the partials of their chunks
+// added in order.  One thread per four columns of a key's row.
+template <int D>
+__global__ void __launch_bounds__(256) attn_bwd_sink_kernel(const BParams p) {
+  griddep_wait();
+  const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // [tile][z][dV, dK][key][D / 4]
+  const int c4 = static_cast<int>(e % (D / 4));
+  const int64_t row = e / (D / 4);  // (tile * BZ + z) * 2 * BT + (dV, dK) * BT + key
+  const int64_t tz = row / (2 * BT);
+  const int in = static_cast<int>(row % (2 * BT));
+  const int j = static_cast<int>(tz / p.BZ), z = static_cast<int>(tz % p.BZ);
+  const int key = j * BT + in % BT;
+  if (j >= p.sink_tiles || key >= p.Sk) return;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const float* src = p.sink_part + ((static_cast<int64_t>(j) * p.sink_chunks * p.BZ + z) * 2 * BT + in) * D + 4 * c4;
+#pragma unroll 4
+  for (int c = 0; c < p.sink_chunks; ++c) {
+    const float4 v = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(c) * p.BZ * 2 * BT * D);
+    acc.x += v.x;
+    acc.y += v.y;
+    acc.z += v.z;
+    acc.w += v.w;
+  }
+  __nv_bfloat16* dst = (in < BT ? p.dv : p.dk) + (static_cast<int64_t>(z) * p.Sk + key) * D + 4 * c4;
+  *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+}
+
+// Window mode: the key tiles query tile i visits, those that hold sinks and are before
+// its window, then the window's.
+struct WinTiles {
+  int n, n_sink, j0;
+  __device__ __forceinline__ int tile(int s) const { return s < n_sink ? s : j0 + s - n_sink; }
+};
+
 // Key tiles query tile i visits: [0, n).
 __device__ __forceinline__ int key_tiles(const BParams& p, int i) {
   if (!p.causal) return p.n_kt;
   const int last_row = min(i * BT + BT, p.Sq) - 1;
   const int kv_end = min(p.Sk, last_row + p.diag + 1);
   return kv_end > 0 ? (kv_end + BT - 1) / BT : 0;
+}
+
+template <bool WINDOW>
+__device__ __forceinline__ WinTiles dq_tiles(const BParams& p, int i) {
+  WinTiles w;
+  const int n_full = key_tiles(p, i);
+  w.n = n_full;
+  w.n_sink = w.j0 = 0;
+  if constexpr (WINDOW) {
+    w.j0 = min(max(i * BT + p.diag - p.window + 1, 0) / BT, n_full);
+    w.n_sink = min(p.sink_tiles, w.j0);
+    w.n = w.n_sink + n_full - w.j0;
+  }
+  return w;
 }
 
 // ---------------------------------------------------------------------------- dQ
@@ -579,7 +704,7 @@ struct QCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
-template <int D>
+template <int D, bool WINDOW = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -643,7 +768,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int x = item_of(k);
       if (x >= p.n_items) continue;
       const int i = p.n_qt - 1 - x / p.BH, bh = x % p.BH;
-      const int n = key_tiles(p, i);
+      const WinTiles wt = dq_tiles<WINDOW>(p, i);
+      const int n = wt.n;
       if (n <= 0) continue;
       if (n_ne > 0) ok = warp_wait(&qd_empty, (n_ne - 1) & 1, abort_v, kTimeoutNs);
       if (!ok) break;
@@ -663,8 +789,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx_elect(&kfull[ks], C::kTileBytes);
 #pragma unroll
         for (int cb = 0; cb < D / 64; ++cb)
-          tma_load_3d_elect(k_ring + ks * C::kTileBytes + cb * BC::kColBlockBytes, &tk, &kfull[ks], cb * 64, j * BT,
-                            kvz);
+          tma_load_3d_elect(k_ring + ks * C::kTileBytes + cb * BC::kColBlockBytes, &tk, &kfull[ks], cb * 64,
+                            wt.tile(j) * BT, kvz);
         if (vl >= VR) ok = warp_wait(&vempty[vs], (vl / VR - 1) & 1, abort_v, kTimeoutNs);
         if (!ok) {
           ++kl;  // the K tile above is in flight
@@ -673,8 +799,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive_expect_tx_elect(&vfull[vs], C::kTileBytes);
 #pragma unroll
         for (int cb = 0; cb < D / 64; ++cb)
-          tma_load_3d_elect(v_ring + vs * C::kTileBytes + cb * BC::kColBlockBytes, &tv, &vfull[vs], cb * 64, j * BT,
-                            kvz);
+          tma_load_3d_elect(v_ring + vs * C::kTileBytes + cb * BC::kColBlockBytes, &tv, &vfull[vs], cb * 64,
+                            wt.tile(j) * BT, kvz);
       }
     }
     if (!ok) {
@@ -741,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k * static_cast<int>(gridDim.x) < p.n_items && ok; ++k) {
       const int x = item_of(k);
       if (x >= p.n_items) continue;
-      const int n = key_tiles(p, p.n_qt - 1 - x / p.BH);
+      const int n = dq_tiles<WINDOW>(p, p.n_qt - 1 - x / p.BH).n;
       if (n <= 0) continue;
       ok = warp_wait(&qd_full, t & 1, abort_v, kTimeoutNs);
       for (int j = 0; j < n && ok; ++j, ++g) {
@@ -788,7 +914,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int x = item_of(k);
       if (x >= p.n_items) continue;
       const int i = p.n_qt - 1 - x / p.BH, bh = x % p.BH;
-      const int n = key_tiles(p, i);
+      const WinTiles wt = dq_tiles<WINDOW>(p, i);
+      const int n = wt.n;
       const int row = i * BT + quarter * 32 + lane;
       const bool live = row < p.Sq;
       __nv_bfloat16* dqrow = p.dq + (static_cast<int64_t>(bh) * p.Sq + row) * D + r * (D / 2);
@@ -815,10 +942,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&dp_free);  // the next step's S and dP may go in
         // keys past kmax (above the diagonal, or past Sk) get S = -inf, hence P = 0 (c > 0)
-        const int kmax = lim - j * BT - BH2 * r;
+        const int k0 = wt.tile(j) * BT + BH2 * r;  // this warpgroup's first key of the step
+        const int kmax = lim - k0;
         if (__any_sync(0xffffffffu, kmax < BH2 - 1)) {
 #pragma unroll
           for (int e = 0; e < 64; ++e) sv[e] = e <= kmax ? sv[e] : __float_as_uint(-INFINITY);
+        }
+        if constexpr (WINDOW) {  // keys before the row's window that are not sinks
+          const int kmin = row + p.diag - p.window + 1 - k0;
+          if (__any_sync(0xffffffffu, kmin > 0) && k0 + BH2 > p.sinks) {
+            const int ksink = p.sinks - k0;
+#pragma unroll
+            for (int e = 0; e < 64; ++e) sv[e] = (e < kmin && e >= ksink) ? __float_as_uint(-INFINITY) : sv[e];
+          }
         }
         // dS = P (dP - D) with P = exp2(S c - LSE log2 e), two keys per packed operation
         uint32_t dsk[32];
@@ -911,9 +1047,14 @@ int prepare_device(int dev) {
   const void* fns[] = {reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<128>),
                        reinterpret_cast<const void*>(attn_bwd_dq_kernel<128>),
                        reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<64>),
-                       reinterpret_cast<const void*>(attn_bwd_dq_kernel<64>)};
-  const int bytes[] = {BCfg<128>::kSmemBytes, QCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes, QCfg<64>::kSmemBytes};
-  for (int f = 0; f < 4 && e == cudaSuccess; ++f)
+                       reinterpret_cast<const void*>(attn_bwd_dq_kernel<64>),
+                       reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<128, true>),
+                       reinterpret_cast<const void*>(attn_bwd_dq_kernel<128, true>),
+                       reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<64, true>),
+                       reinterpret_cast<const void*>(attn_bwd_dq_kernel<64, true>)};
+  const int bytes[] = {BCfg<128>::kSmemBytes, QCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes, QCfg<64>::kSmemBytes,
+                       BCfg<128>::kSmemBytes, QCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes, QCfg<64>::kSmemBytes};
+  for (int f = 0; f < 8 && e == cudaSuccess; ++f)
     e = cudaFuncSetAttribute(fns[f], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[f]);
   if (e != cudaSuccess) return cuda_fail(e);
   if (!attn_host::encode_tiled_fn()) return ATTN_ERR_TENSOR_MAP;
@@ -931,7 +1072,27 @@ bool misaligned(const void* ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15
 
 int64_t padded_rows(int Sq) { return (static_cast<int64_t>(Sq) + BT - 1) / BT * BT; }
 
-template <int D>
+// Window mode: how the dK/dV work of the key tiles that hold sinks is cut.  Such a tile is
+// seen by every later query tile, a tile without sinks by about window / 128 + 2 of them;
+// chunks of that many query tiles (eight at least) make the items about equal.
+struct SinkPlan {
+  int tiles, chunks, per;
+  size_t bytes;  // of the fp32 partials
+};
+
+constexpr int kMaxSinkChunks = 64;
+
+SinkPlan sink_plan(int64_t BZ, int Sq, int Sk, int D, int window, int sinks) {
+  SinkPlan s;
+  s.tiles = (std::min(sinks, Sk) + BT - 1) / BT;
+  const int n_qt = static_cast<int>(padded_rows(Sq) / BT);
+  s.per = std::max({window / BT + 2, 8, (n_qt + kMaxSinkChunks - 1) / kMaxSinkChunks});
+  s.chunks = s.tiles > 0 ? std::max((n_qt + s.per - 1) / s.per, 1) : 1;
+  s.bytes = s.chunks > 1 ? static_cast<size_t>(s.tiles) * s.chunks * BZ * 2 * BT * D * 4 : 0;
+  return s;
+}
+
+template <int D, bool WINDOW>
 int launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
                BParams prm, const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse, float* lse2,
                float* delta, int sms, cudaStream_t stream) {
@@ -953,31 +1114,34 @@ int launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   BParams a = prm;
-  a.n_items = prm.n_kt * prm.BZ;
+  a.n_items = WINDOW ? (prm.n_kt + prm.sink_tiles * (prm.sink_chunks - 1)) * prm.BZ : prm.n_kt * prm.BZ;
   cfg.gridDim = dim3(a.n_items < sms ? a.n_items : sms);
-  e = cudaLaunchKernelEx(&cfg, attn_bwd_dkdv_kernel<D>, tq, tk, tv, tdo, a);
+  e = cudaLaunchKernelEx(&cfg, attn_bwd_dkdv_kernel<D, WINDOW>, tq, tk, tv, tdo, a);
   if (e != cudaSuccess) return cuda_fail(e);
   BParams b = prm;
   b.n_items = prm.n_qt * prm.BH;
   cfg.gridDim = dim3(b.n_items < sms ? b.n_items : sms);
   cfg.dynamicSmemBytes = QCfg<D>::kSmemBytes;
-  e = cudaLaunchKernelEx(&cfg, attn_bwd_dq_kernel<D>, tq, tk, tv, tdo, b);
+  e = cudaLaunchKernelEx(&cfg, attn_bwd_dq_kernel<D, WINDOW>, tq, tk, tv, tdo, b);
+  if (WINDOW && e == cudaSuccess && prm.sink_tiles > 0 && prm.sink_chunks > 1) {
+    const int64_t quads = static_cast<int64_t>(prm.sink_tiles) * prm.BZ * 2 * BT * (D / 4);
+    cfg.gridDim = dim3(static_cast<unsigned>((quads + 255) / 256));
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, attn_bwd_sink_kernel<D>, prm);
+  }
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
 
-}  // namespace
-
-extern "C" {
-
-size_t attn_bwd_workspace_size(int B, int Hq, int Sq) {
-  if (B < 0 || Hq < 1 || Sq < 0) return 0;
+size_t vector_bytes(int B, int Hq, int Sq) {
   const size_t one = static_cast<size_t>(B) * Hq * padded_rows(Sq) * 4;
   return 2 * ((one + 255) & ~static_cast<size_t>(255));
 }
 
-int attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
-             void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale,
-             void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+// attn_bwd (window == 0) and attn_bwd_window.
+int run_backward(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                 void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, int window,
+                 int sinks, float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   // ---- argument checks (host only, before any CUDA call)
   if (B < 0 || Sq < 0 || Sk < 0 || Hq < 1 || Hkv < 1) return ATTN_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return ATTN_ERR_INVALID_ARG;
@@ -986,7 +1150,9 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* o, const f
   if (B == 0) return ATTN_OK;
   const size_t qb = static_cast<size_t>(B) * Hq * Sq * D * 2, kb = static_cast<size_t>(B) * Hkv * Sk * D * 2;
   const size_t lb = static_cast<size_t>(B) * Hq * Sq * 4;
-  const size_t wb = attn_bwd_workspace_size(B, Hq, Sq);
+  const size_t vb = vector_bytes(B, Hq, Sq);
+  const SinkPlan sink = sink_plan(static_cast<int64_t>(B) * Hkv, Sq, Sk, D, window, sinks);
+  const size_t wb = vb + sink.bytes;
   if (Sq > 0 && (!q || !o || !lse || !dout || !dq)) return ATTN_ERR_NULL_PTR;
   if (Sk > 0 && (!k || !v || !dk || !dv)) return ATTN_ERR_NULL_PTR;
   if (Sq > 0 && Sk > 0 && !workspace) return ATTN_ERR_NULL_PTR;
@@ -1032,7 +1198,7 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* o, const f
   prm.dq = static_cast<__nv_bfloat16*>(dq);
   prm.dk = static_cast<__nv_bfloat16*>(dk);
   prm.dv = static_cast<__nv_bfloat16*>(dv);
-  const size_t one = wb / 2;
+  const size_t one = vb / 2;
   float* lse2 = static_cast<float*>(workspace);  // stored negated, as the kernels use them
   float* delta = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + one);
   prm.nlse2 = lse2;
@@ -1052,10 +1218,50 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* o, const f
   prm.n_items = 0;
   prm.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   prm.scale = scale;
+  prm.window = std::min(window, std::max(Sq, Sk));  // no visible key is further away
+  prm.sinks = std::min(sinks, Sk);
+  prm.sink_tiles = sink.tiles;
+  prm.sink_chunks = sink.chunks;
+  prm.sink_per = sink.per;
+  prm.sink_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + vb);
   const auto* ob = static_cast<const __nv_bfloat16*>(o);
   const auto* gb = static_cast<const __nv_bfloat16*>(dout);
-  return D == 128 ? launch_all<128>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, g_dev_sms[dev], stream)
-                  : launch_all<64>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, g_dev_sms[dev], stream);
+  const int sms = g_dev_sms[dev];
+  if (window > 0)
+    return D == 128 ? launch_all<128, true>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, sms, stream)
+                    : launch_all<64, true>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, sms, stream);
+  return D == 128 ? launch_all<128, false>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, sms, stream)
+                  : launch_all<64, false>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, sms, stream);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t attn_bwd_workspace_size(int B, int Hq, int Sq) {
+  if (B < 0 || Hq < 1 || Sq < 0) return 0;
+  return vector_bytes(B, Hq, Sq);
+}
+
+int attn_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+             void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal, float scale,
+             void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return run_backward(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, causal, 0, 0, scale, workspace,
+                      workspace_bytes, stream);
+}
+
+size_t attn_bwd_window_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks) {
+  if (B < 0 || Hq < 1 || Hkv < 1 || Sq < 0 || Sk < 0 || (D != 64 && D != 128) || window < 1 || sinks < 0) return 0;
+  return vector_bytes(B, Hq, Sq) + sink_plan(static_cast<int64_t>(B) * Hkv, Sq, Sk, D, window, sinks).bytes;
+}
+
+int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                    void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal,
+                    int window, int sinks, float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  if (causal != 1 && causal != 2) return ATTN_ERR_INVALID_ARG;
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  return run_backward(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, Sq, Sk, D, causal, window, sinks, scale,
+                      workspace, workspace_bytes, stream);
 }
 
 const char* attn_bwd_strerror(int status) {

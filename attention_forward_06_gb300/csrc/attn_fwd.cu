@@ -152,6 +152,9 @@ struct Params {
   const int32_t* order;
   int order_heads;  // 1 (one order for every head) or Hq
   int order_len;    // entries per row: ceil(Sk / 128)
+  // window mode: key j also needs row + diag - j < window or j < sinks
+  int window;  // 1 .. max(Sq, Sk)
+  int sinks;   // 0 .. Sk
 };
 
 struct Item {
@@ -161,6 +164,7 @@ struct Item {
   int j0;       // first key tile
   int n_tiles;  // key tiles to visit
   int split;    // key range index (split-key mode)
+  int n_sink;   // window mode: the first n_sink tiles visited are key tiles 0 .. n_sink - 1, the rest start at j0
 };
 
 // Item x of the heaviest-first list: query block from the last, then (split-key
@@ -169,7 +173,7 @@ struct Item {
 // adjacent -- kv heads in order, then query blocks from the last, the group's
 // query heads fastest -- so they run side by side and share each K and V tile
 // through L2.
-template <bool SPLIT, bool SPARSE = false, bool GROUPED = false>
+template <bool SPLIT, bool SPARSE = false, bool GROUPED = false, bool WINDOW = false>
 __device__ __forceinline__ Item item_at(const Params& p, int x) {
   Item it;
   int qb, r;
@@ -203,12 +207,21 @@ __device__ __forceinline__ Item item_at(const Params& p, int x) {
   if (SPLIT) {
     it.j0 = static_cast<int>(static_cast<int64_t>(it.split) * n_full / p.n_splits);
     it.n_tiles = static_cast<int>(static_cast<int64_t>(it.split + 1) * n_full / p.n_splits) - it.j0;
+  } else if (WINDOW) {
+    // the tiles from the first key any row of the item has in its window, and before
+    // them the tiles that hold sinks and are not among those
+    it.j0 = min(max(it.q0 + p.diag - p.window + 1, 0) / BN, n_full);
+    it.n_sink = min((max(min(p.sinks, kv_end), 0) + BN - 1) / BN, it.j0);
+    it.n_tiles = it.n_sink + n_full - it.j0;
   } else {
     it.j0 = 0;
     it.n_tiles = n_full;  // block-sparse mode: the causal bound; the producer counts the marked tiles
   }
   return it;
 }
+
+// Window mode: the key tile of an item's step i.
+__device__ __forceinline__ int window_tile(const Item& it, int i) { return i < it.n_sink ? i : it.j0 + i - it.n_sink; }
 
 // Block-sparse mode: the two mask rows of an item (its Q tiles' query blocks; a Q
 // tile past the last query block has none), word w of their union clipped to the
@@ -397,7 +410,7 @@ __device__ __forceinline__ void record_abort(volatile uint32_t* abort_flag, int 
   atomicCAS(&g_status, 0, site);
 }
 
-template <int D, bool SPLIT, bool SPARSE, bool ORDERED = false, bool GROUPED = false>
+template <int D, bool SPLIT, bool SPARSE, bool ORDERED = false, bool GROUPED = false, bool WINDOW = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                     const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap to,
@@ -409,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool LISTED = SPARSE || ORDERED;
   static_assert(!(SPARSE && ORDERED) && !(SPLIT && (SPARSE || ORDERED)), "one visiting mode at a time");
   static_assert(!GROUPED || !SPLIT, "the grouped order lists whole-key-range items");
+  static_assert(!WINDOW || !(SPLIT || LISTED || GROUPED), "the window mode has its own tile list");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
   uint8_t* q_s = smem;               // Q tile t at q_s + t * kTileBytes
@@ -503,9 +517,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       int n_marked = 0;  // block-sparse / ordered mode: the key tiles the item visits
       if constexpr (SPARSE) {
-        if (more) n_marked = sparse_tiles(p, item_at<SPLIT, SPARSE, GROUPED>(p, x));
+        if (more) n_marked = sparse_tiles(p, item_at<SPLIT, SPARSE, GROUPED, WINDOW>(p, x));
       } else if constexpr (ORDERED) {
-        if (more) n_marked = ordered_tiles(p, item_at<SPLIT, false, GROUPED>(p, x));
+        if (more) n_marked = ordered_tiles(p, item_at<SPLIT, false, GROUPED, WINDOW>(p, x));
       }
       if (lane == 0) {
         item_seq[k % kSeqSlots] = more ? x : -1;
@@ -515,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       ATTN_TR(1, more ? x : -1);  // item published
       if (!more) break;
-      const Item it = item_at<SPLIT, SPARSE, GROUPED>(p, x);
+      const Item it = item_at<SPLIT, SPARSE, GROUPED, WINDOW>(p, x);
       const int n_tiles = LISTED ? n_marked : it.n_tiles;
       // The next item is claimed once this item's loads are all issued (about two
       // key tiles before its end), so items are handed out in the order CTAs free up.
@@ -571,6 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         } else if constexpr (ORDERED) {
           if (!(i & 1)) kb = owalk.next();  // the next tile of the order
+        } else if constexpr (WINDOW) {
+          kb = window_tile(it, i >> 1);
         } else {
           kb = it.j0 + (i >> 1);
         }
@@ -646,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int x, n_marked = 0;
       ok = next_item(k, x, LISTED ? &n_marked : nullptr);
       if (!ok || x < 0) break;
-      const int n = LISTED ? n_marked : item_at<SPLIT, false, GROUPED>(p, x).n_tiles;
+      const int n = LISTED ? n_marked : item_at<SPLIT, false, GROUPED, WINDOW>(p, x).n_tiles;
       if (n == 0) continue;
       ok = warp_wait(&q_full, n_done & 1, abort_v, kTimeoutNs);
       if (ok) ok = wait_kv(kv_it);
@@ -770,7 +786,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = next_item(k, x, LISTED ? &n_marked : nullptr);
       if (!ok || x < 0) break;
       if constexpr (!SPLIT) {  // split-key partials are written by the softmax warps directly
-        const Item it = item_at<SPLIT, SPARSE, GROUPED>(p, x);
+        const Item it = item_at<SPLIT, SPARSE, GROUPED, WINDOW>(p, x);
         if ((LISTED ? n_marked : it.n_tiles) == 0) continue;
         for (int t = 0; t < QTILES && ok; ++t) {
           ok = warp_wait(&stage_full[t], e_seen[t] & 1, abort_v, kTimeoutNs);
@@ -815,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       if (x < 0) break;
-      const Item it = item_at<SPLIT, SPARSE, GROUPED>(p, x);
+      const Item it = item_at<SPLIT, SPARSE, GROUPED, WINDOW>(p, x);
       const int n_tiles = LISTED ? n_marked : it.n_tiles;  // key tiles the item visits
       const int row = it.q0 + t * BM + quarter * 32 + lane;  // global query row
       const bool live = row < p.Sq;
@@ -846,6 +862,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         lim = min(lim, row + p.diag);
         lim_tile = min(lim_tile, tile_row0 + p.diag);
       }
+      // window mode: first key of this row's window, and of the tile's last row (the most restricted)
+      const int low = WINDOW ? row + p.diag - p.window + 1 : 0;
+      const int low_tile = WINDOW ? tile_row0 + BM - 1 + p.diag - p.window + 1 : 0;
       float m = -INFINITY;   // running max, log2 units
       float l = 0.0f;        // sum of the fp16-rounded P the tensor cores use (normalises O)
       float l_exact = 0.0f;  // sum of the fp32 P (gives LSE)
@@ -878,10 +897,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           mcur &= mcur - 1;
         } else if constexpr (ORDERED) {
           jg = owalk.next();
+        } else if constexpr (WINDOW) {
+          jg = window_tile(it, j);
         }
         // the tile is unmarked for this Q tile, or straddles the diagonal or the end of K
         const bool masked = !own || jg * BN + BN - 1 > lim_tile;
         const int kmax = own ? lim - jg * BN : -1;
+        // window mode: keys before kmin that are not sinks (from ksink on) are out of the row's window
+        const bool masked_low = WINDOW && jg * BN < low_tile && jg * BN + BN > p.sinks;
+        const int kmin = WINDOW ? low - jg * BN : 0;
+        const int ksink = WINDOW ? p.sinks - jg * BN : 0;
         // V of this tile (load 2g + 1 of the CTA's K/V stream) to fp16, in place in its ring
         // slot: the 256 softmax threads take one 16-byte chunk in 256 each (a chunk holds 8
         // consecutive values of one row, so the swizzled layout is unchanged), make their
@@ -915,11 +940,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         ATTN_TR(20, j);  // S_t(j) ready
         tc_fence_after();
-        if constexpr (SPARSE) {
-          // block-sparse mode: a tile no row of this warp sees (one only the other Q tile's
-          // query block marks, or one past this tile's causal limit) has P = 0, written
-          // without reading S or taking an exponential
-          if (__all_sync(0xffffffffu, kmax < 0)) {
+        if constexpr (SPARSE || WINDOW) {
+          // block-sparse and window mode: a tile no row of this warp sees (one only the other
+          // Q tile's query block marks, one past this tile's causal limit, or one wholly before
+          // every row's window) has P = 0, written without reading S or taking an exponential
+          if (__all_sync(0xffffffffu, kmax < 0 || (masked_low && kmin >= BN && ksink <= 0))) {
             uint32_t z[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] = 0u;
@@ -937,6 +962,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (masked) {
 #pragma unroll
           for (int i = 0; i < 128; ++i) r[i] = (i > kmax) ? __float_as_uint(-INFINITY) : r[i];
+        }
+        if constexpr (WINDOW) {
+          if (masked_low) {
+            const int k0 = max(ksink, 0);  // keys k0 .. kmin - 1 of the tile are masked
+#pragma unroll
+            for (int i = 0; i < 128; ++i) r[i] = (i < kmin && i >= k0) ? __float_as_uint(-INFINITY) : r[i];
+          }
         }
         const float m_in = m;  // the reference value the tile starts from
         // Row max of the tile; when it exceeds m, m moves kHeadroom above it.
@@ -1037,6 +1069,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) {
               s0[i] = (masked && i > kmax) ? __float_as_uint(-INFINITY) : s0[i];
               s1[i] = (masked && 32 + i > kmax) ? __float_as_uint(-INFINITY) : s1[i];
+              if constexpr (WINDOW) {
+                s0[i] = (masked_low && i < kmin && i >= ksink) ? __float_as_uint(-INFINITY) : s0[i];
+                s1[i] = (masked_low && 32 + i < kmin && 32 + i >= ksink) ? __float_as_uint(-INFINITY) : s1[i];
+              }
               mx = max3f(mx, __uint_as_float(s0[i]), __uint_as_float(s1[i]));
             }
 #pragma unroll
@@ -1254,14 +1290,16 @@ int prepare_device(int dev) {
                         reinterpret_cast<const void*>(attn_fwd_kernel<128, false, false, true>),
                         reinterpret_cast<const void*>(attn_fwd_kernel<128, false, false, false, true>),
                         reinterpret_cast<const void*>(attn_fwd_kernel<128, false, true, false, true>),
-                        reinterpret_cast<const void*>(attn_fwd_kernel<128, false, false, true, true>)};
+                        reinterpret_cast<const void*>(attn_fwd_kernel<128, false, false, true, true>),
+                        reinterpret_cast<const void*>(attn_fwd_kernel<128, false, false, false, false, true>)};
   const void* k64[] = {reinterpret_cast<const void*>(attn_fwd_kernel<64, false, false>),
                        reinterpret_cast<const void*>(attn_fwd_kernel<64, true, false>),
                        reinterpret_cast<const void*>(attn_fwd_kernel<64, false, true>),
                        reinterpret_cast<const void*>(attn_fwd_kernel<64, false, false, true>),
                        reinterpret_cast<const void*>(attn_fwd_kernel<64, false, false, false, true>),
                        reinterpret_cast<const void*>(attn_fwd_kernel<64, false, true, false, true>),
-                       reinterpret_cast<const void*>(attn_fwd_kernel<64, false, false, true, true>)};
+                       reinterpret_cast<const void*>(attn_fwd_kernel<64, false, false, true, true>),
+                       reinterpret_cast<const void*>(attn_fwd_kernel<64, false, false, false, false, true>)};
   for (const void* f : k128)
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::kSmemBytes);
@@ -1420,6 +1458,8 @@ int prepare_launch(const void* q, const void* k, const void* v, void* o, float* 
   prm.order_len = 0;
   prm.mask_heads = 1;
   prm.mask_words = 0;
+  prm.window = 1;
+  prm.sinks = 0;
   prm.n_qtiles = static_cast<int>((Sq + BM - 1) / BM);
   // persistent: one CTA per SM (shared memory and TMEM allow no second), never more CTAs than items
   L->grid = static_cast<int>(items < g_dev_sms[L->dev] ? items : g_dev_sms[L->dev]);
@@ -1440,9 +1480,9 @@ int prepare_launch(const void* q, const void* k, const void* v, void* o, float* 
   return ATTN_OK;
 }
 
-template <int D, bool SPLIT, bool SPARSE = false, bool ORDERED = false, bool GROUPED = false>
+template <int D, bool SPLIT, bool SPARSE = false, bool ORDERED = false, bool GROUPED = false, bool WINDOW = false>
 int launch(const Launch& L, cudaStream_t stream) {
-  attn_fwd_kernel<D, SPLIT, SPARSE, ORDERED, GROUPED><<<L.grid, kThreads, Cfg<D>::kSmemBytes, stream>>>(
+  attn_fwd_kernel<D, SPLIT, SPARSE, ORDERED, GROUPED, WINDOW><<<L.grid, kThreads, Cfg<D>::kSmemBytes, stream>>>(
       L.tq, L.tk, L.tv, L.to, L.prm);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
@@ -1648,6 +1688,20 @@ int attn_fwd_blocksparse(const void* q, const void* k, const void* v, void* o, f
   if (L.grouped)
     return D == 128 ? launch<128, false, true, false, true>(L, stream) : launch<64, false, true, false, true>(L, stream);
   return D == 128 ? launch<128, false, true>(L, stream) : launch<64, false, true>(L, stream);
+}
+
+int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Sq,
+                    int Sk, int D, int causal, int window, int sinks, float scale, cudaStream_t stream) {
+  // the window's own checks (host only, before any CUDA call), then the common ones
+  if (causal != 1 && causal != 2) return ATTN_ERR_INVALID_ARG;
+  if (window < 1 || sinks < 0) return ATTN_ERR_INVALID_ARG;
+  Launch L;
+  const int st = prepare_launch(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, D, causal, scale, 1, stream, &L);
+  if (st != ATTN_OK || L.empty) return st;
+  L.prm.window = std::min(window, std::max(std::max(Sq, Sk), 1));  // no visible key is further away
+  L.prm.sinks = std::min(sinks, Sk);
+  return D == 128 ? launch<128, false, false, false, false, true>(L, stream)
+                  : launch<64, false, false, false, false, true>(L, stream);
 }
 
 size_t attn_fwd_tile_order_entries(int B, int order_heads, int Sq, int Sk) {

@@ -238,6 +238,65 @@ def attn_fwd_ordered(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tile_ord
     return o, lse
 
 
+def _on_device(**tensors) -> torch.device:
+    """The one CUDA device that all of the given tensors (None: absent) lie on, which has to be the current one."""
+    dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the tensors before it on {dev}")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
+    return dev
+
+
+def _window_shapes(q, k, v, window, sinks, causal):
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.dim() != 4:
+            raise ValueError(f"{name} must be a contiguous 4-d bf16 CUDA tensor")
+    if v.shape != k.shape or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
+        raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
+    if causal not in (1, 2):
+        raise ValueError("causal must be 1 (bottom-right) or 2 (top-left)")
+    if window < 1 or sinks < 0:
+        raise ValueError("window must be at least 1 and sinks at least 0")
+    return (*q.shape[:2], k.shape[1], q.shape[2], k.shape[2], q.shape[3])
+
+
+_INT_MAX = 2 ** 31 - 1
+
+
+def attn_fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0, causal: int = 1,
+                    scale: float | None = None, o: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    stream=None):
+    """Sliding-window forward with sink tokens: ``(o, lse)``.
+
+    ``attn_fwd`` with key j visible to row i iff ``j <= p_i`` and (``p_i - j < window`` or ``j < sinks``), where
+    ``p_i`` is ``i + Sk - Sq`` (causal 1) or ``i`` (causal 2).  A row without keys gets ``o = 0``, ``lse = -inf``.
+    """
+    B, Hq, Hkv, Sq, Sk, D = _window_shapes(q, k, v, window, sinks, causal)
+    _on_device(q=q, k=k, v=v, o=o, lse=lse)
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    if o is None:
+        o = torch.empty_like(q)
+    elif o.shape != q.shape or o.dtype != torch.bfloat16 or not o.is_contiguous():
+        raise ValueError("o must be a contiguous bf16 tensor shaped like q")
+    if lse is None:
+        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
+    elif tuple(lse.shape) != (B, Hq, Sq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, Sq]")
+    _check(load().attn_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
+                                  Sq, Sk, D, int(causal), min(int(window), _INT_MAX), min(int(sinks), _INT_MAX),
+                                  float(scale), _stream_handle(stream)))
+    return o, lse
+
+
 def bwd_workspace_size(B: int, Hq: int, Sq: int) -> int:
     return int(load("attn_bwd").attn_bwd_workspace_size(B, Hq, Sq))
 
@@ -272,6 +331,49 @@ def attn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
     st = lib.attn_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                       dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Sk, D, int(causal),
                       ctypes.c_float(scale), workspace.data_ptr(), ws_bytes, _stream_handle(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, lib.attn_bwd_strerror(st).decode())
+    return dq, dk, dv
+
+
+def bwd_window_workspace_size(B: int, Hq: int, Hkv: int, Sq: int, Sk: int, D: int, window: int, sinks: int) -> int:
+    return int(load("attn_bwd").attn_bwd_window_workspace_size(B, Hq, Hkv, Sq, Sk, D, min(int(window), _INT_MAX),
+                                                               min(int(sinks), _INT_MAX)))
+
+
+def attn_bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor,
+                    dout: torch.Tensor, window: int, sinks: int = 0, causal: int = 1, scale: float | None = None,
+                    dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None):
+    """Backward of ``attn_fwd_window``: ``(dq, dk, dv)`` for the upstream gradient ``dout`` of ``o``.
+
+    ``o`` and ``lse`` are the forward's outputs for the same ``q, k, v, window, sinks, causal, scale``.
+    ``workspace`` (a contiguous CUDA tensor of at least ``bwd_window_workspace_size`` bytes) is allocated here
+    when not given.
+    """
+    B, Hq, Hkv, Sq, Sk, D = _window_shapes(q, k, v, window, sinks, causal)
+    _on_device(q=q, k=k, v=v, o=o, lse=lse, dout=dout, dq=dq, dk=dk, dv=dv, workspace=workspace)
+    for name, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
+        if t is not None and (t.dtype != torch.bfloat16 or t.shape != like.shape or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous bf16 tensor of shape {tuple(like.shape)}")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, Sq) or not lse.is_contiguous():
+        raise ValueError("lse must be the forward's contiguous fp32 [B, Hq, Sq]")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    if workspace is None:
+        need = bwd_window_workspace_size(B, Hq, Hkv, Sq, Sk, D, window, sinks)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    lib = load("attn_bwd")
+    st = lib.attn_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
+                             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Sk, D, int(causal),
+                             min(int(window), _INT_MAX), min(int(sinks), _INT_MAX), float(scale),
+                             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                             _stream_handle(stream))
     if st != ATTN_OK:
         raise AttnError(st, lib.attn_bwd_strerror(st).decode())
     return dq, dk, dv

@@ -224,6 +224,27 @@ int attn_fwd_ordered(const void* q, const void* k, const void* v, void* o, float
    invalid sizes.  Host only, no CUDA call. */
 size_t attn_fwd_tile_order_entries(int B, int order_heads, int Sq, int Sk);
 
+/*
+ * Sliding-window forward with sink tokens: attn_fwd restricted to the keys near
+ * each row and the first `sinks` keys.  With p_i = i + (Sk - Sq) (causal 1) or i
+ * (causal 2), key j is visible to row i iff
+ *     j <= p_i   and   (p_i - j < window   or   j < sinks),
+ * so a row sees itself and the window - 1 keys before it, and the first keys of
+ * the sequence stay visible at any distance.  Key tiles no row of a 256-row query
+ * block sees are never loaded: the work grows with Sq * (window + sinks), not
+ * Sq * Sk.  A row with no visible key gets O = 0 and LSE = -inf; a window of at
+ * least max(Sq, Sk) gives attn_fwd's result.
+ *
+ * causal is 1 or 2, window >= 1, sinks >= 0 (ATTN_ERR_INVALID_ARG otherwise);
+ * other arguments, layouts and status codes as attn_fwd.  One kernel is enqueued
+ * on `stream`; nothing is allocated.  The work order is heads fastest always
+ * (consecutive query blocks share most of their window through L2), and
+ * ATTN_FWD_ITEM_ORDER does not apply.  attn_bwd_window (attn_bwd.h) is its
+ * backward; attn_fwd_tree (attn_paged.h) its form for single tokens over a cache.
+ */
+int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Sq,
+                    int Sk, int D, int causal, int window, int sinks, float scale, cudaStream_t stream);
+
 /* Text for a status code.  For ATTN_ERR_CUDA it names the CUDA error of the
    calling thread's most recent failing call. */
 const char* attn_fwd_strerror(int status);
