@@ -16,8 +16,20 @@ _libs: dict[str, ctypes.CDLL] = {}
 
 _c_int, _c_float, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
 
+
+class KvCache(ctypes.Structure):
+    """attn_kv_cache of include/attn_kv.h."""
+
+    _fields_ = ([("k", _vp), ("v", _vp)]
+                + [(f"{t}_stride_{d}", ctypes.c_int64) for t in "kv" for d in ("page", "head", "slot")]
+                + [(n, _vp) for n in ("page_table", "seq_lens", "ref_counts")]
+                + [(n, ctypes.c_int32) for n in ("n_pages", "Hkv", "page_size", "D", "rows", "max_pages")])
+
+
+_cache, _i64 = ctypes.POINTER(KvCache), ctypes.c_int64
+
 # name -> (restype, argtypes), mirroring include/attn_fwd.h, include/attn_fwd_trace.h, include/attn_bwd.h,
-# include/attn_bwd_trace.h and include/attn_fwd_probe.h
+# include/attn_bwd_trace.h, include/attn_kv.h and include/attn_fwd_probe.h
 SIGNATURES = {
     "attn_fwd": {
         "attn_fwd": (_c_int, [_vp, _vp, _vp, _vp, _vp] + [_c_int] * 7 + [_c_float, _vp]),
@@ -43,6 +55,13 @@ SIGNATURES = {
         "attn_bwd_window_workspace_size": (ctypes.c_size_t, [_c_int] * 8),
         "attn_bwd_strerror": (ctypes.c_char_p, [_c_int]),
         "attn_bwd_debug_status": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
+    },
+    "attn_kv": {
+        "attn_kv_append": (_c_int, [_cache, _vp, _vp, _i64, _i64, _i64, _i64, _c_int, _vp, _vp, _vp]),
+        "attn_kv_fork": (_c_int, [_cache, _vp, _vp, _c_int, _vp, _vp]),
+        "attn_kv_compact": (_c_int, [_cache, _vp, _vp, _c_int, _vp, _vp, _vp]),
+        "attn_kv_free": (_c_int, [_cache, _vp, _c_int, _vp]),
+        "attn_kv_strerror": (ctypes.c_char_p, [_c_int]),
     },
     "attn_probe": {
         "attn_probe_mma_ss": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp]),

@@ -1,0 +1,93 @@
+// kv_host.h -- host-side checks shared by the calls on a paged cache (attn_kv.h's
+// layout): the current device, and the cache's sizes, strides and pointers.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <mutex>
+
+#include "attn_kv.h"
+
+namespace attn_host {
+
+inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// One (page, head, slot) tensor: no two elements in one place (each dimension steps past
+// everything the smaller ones span), rows of D on 16-byte boundaries.
+inline bool strides_ok(int64_t page, int64_t head, int64_t slot, const attn_kv_cache& c) {
+  struct Dim {
+    int64_t stride, size;
+  } d[3] = {{page, c.n_pages}, {head, c.Hkv}, {slot, c.page_size}};
+  std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return a.stride < b.stride; });
+  int64_t span = c.D;
+  for (const Dim& x : d) {
+    if (x.size <= 1) continue;
+    if (x.stride % 8 != 0 || x.stride < span) return false;
+    if (x.stride > (INT64_MAX / 4) / x.size) return false;
+    span = x.stride * x.size;
+  }
+  return true;
+}
+
+// The cache's own arguments; `pool`: the call reads or writes k and v.
+inline int check_cache(const attn_kv_cache* c, bool pool, bool counts) {
+  if (!c) return ATTN_ERR_NULL_PTR;
+  if (c->D != 64 && c->D != 128) return ATTN_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return ATTN_ERR_INVALID_ARG;
+  if (c->Hkv < 1 || c->rows < 0 || c->rows > ATTN_KV_MAX_ROWS || c->n_pages < 0 || c->n_pages > ATTN_KV_MAX_PAGES ||
+      c->max_pages < 0 || static_cast<int64_t>(c->max_pages) * c->page_size > INT32_MAX)
+    return ATTN_ERR_INVALID_ARG;
+  if (c->rows > 0 && (!c->seq_lens || (c->max_pages > 0 && !c->page_table))) return ATTN_ERR_NULL_PTR;
+  if (counts && c->n_pages > 0 && !c->ref_counts) return ATTN_ERR_NULL_PTR;
+  if (!aligned_to(c->page_table, 4) || !aligned_to(c->seq_lens, 4) || !aligned_to(c->ref_counts, 4))
+    return ATTN_ERR_MISALIGNED;
+  if (pool && c->n_pages > 0) {
+    if (!c->k || !c->v) return ATTN_ERR_NULL_PTR;
+    if (!aligned_to(c->k, 16) || !aligned_to(c->v, 16)) return ATTN_ERR_MISALIGNED;
+    if (!strides_ok(c->k_stride_page, c->k_stride_head, c->k_stride_slot, *c) ||
+        !strides_ok(c->v_stride_page, c->v_stride_head, c->v_stride_slot, *c))
+      return ATTN_ERR_INVALID_ARG;
+  }
+  return ATTN_OK;
+}
+
+// The current device's number of multiprocessors: positive; 0 when it is not sm_103a; or
+// -1 when a CUDA call failed (`*err`).
+inline int device_sms(cudaError_t* err, int* dev_out = nullptr) {
+  constexpr int kMax = 64;
+  static std::mutex mutex;
+  static int sms[kMax];  // 0: not asked yet, -1: another architecture
+  int dev = 0;
+  *err = cudaGetDevice(&dev);
+  if (*err != cudaSuccess) return -1;
+  if (dev_out) *dev_out = dev;
+  if (dev < 0 || dev >= kMax) return 0;
+  std::lock_guard<std::mutex> lock(mutex);
+  if (sms[dev] == 0) {
+    int major = 0, minor = 0, n = 0;
+    *err = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    if (*err == cudaSuccess) *err = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+    if (*err == cudaSuccess) *err = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (*err != cudaSuccess) return -1;
+    sms[dev] = major == 10 && minor == 3 ? n : -1;
+  }
+  return std::max(sms[dev], 0);
+}
+
+inline const char* status_text(int status, cudaError_t last) {
+  switch (status) {
+    case ATTN_OK: return "success";
+    case ATTN_ERR_INVALID_ARG: return "invalid argument";
+    case ATTN_ERR_NULL_PTR: return "null pointer";
+    case ATTN_ERR_MISALIGNED: return "pointer not aligned";
+    case ATTN_ERR_UNSUPPORTED_DEVICE: return "device is not compute capability 10.3 (sm_103a)";
+    case ATTN_ERR_CUDA: return cudaGetErrorString(last);
+    case ATTN_ERR_DEVICE_TIMEOUT: return "a kernel wait ran out of time; the kernel unwound";
+    case ATTN_ERR_TENSOR_MAP: return "TMA tensor map rejected by the driver";
+    default: return "unknown status";
+  }
+}
+
+}  // namespace attn_host

@@ -1,0 +1,567 @@
+// kv_pages.cu -- the calls that change a paged key/value cache (attn_kv.h): append,
+// fork, compact, free.  Nothing is computed; the bound is the bytes moved (each row
+// read once and written once) and, for the few rows of a serving step, the chain of
+// dependent loads and the launches.  So each call is one kernel, or a planning kernel
+// of one block and a moving kernel that starts under it (programmatic dependent
+// launch).
+//
+// Pages are handed out by one block: an exclusive sum over the rows gives each row
+// its place in the order of requests, a second one over the reference counts numbers the free
+// pages, and free page k goes to the row whose requests cover k (binary search).
+// There is no list of free pages to keep in step: a count of 0 is a free page.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "attn_kv.h"
+#include "kv_host.h"
+#include "ptx.cuh"
+
+using namespace attn;
+
+namespace {
+
+constexpr int kPlan = 1024;  // threads of a planning block
+constexpr int kScan = 4;     // reference counts per thread and step
+
+__device__ __forceinline__ int pages_of(int tokens, int page_size) { return (tokens + page_size - 1) / page_size; }
+
+// Exclusive sum of v over the block (kPlan threads) and its total.
+template <class T>
+__device__ __forceinline__ T block_scan(T v, T& total) {
+  __shared__ T warp_sum[32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  T x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const T y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();  // the previous call's readers are done
+  if (lane == 31) warp_sum[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    T w = warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const T y = __shfl_up_sync(0xffffffffu, w, d);
+      if (lane >= d) w += y;
+    }
+    warp_sum[lane] = w;
+  }
+  __syncthreads();
+  total = warp_sum[31];
+  return x - v + (warp ? warp_sum[warp - 1] : T{0});
+}
+
+// Requests of `count` takers: need(i) pages each (the block calls it with every i once, in
+// order).  off[i] (shared memory) becomes the number of pages asked before taker i,
+// saturated (then there are not as many).  Returns the total; `bad` is true in every
+// thread if need(i) was negative anywhere.
+template <class Need>
+__device__ __forceinline__ uint64_t sum_requests(int count, uint32_t* off, bool& bad, Need need) {
+  uint64_t carry = 0;
+  bool mine = false;
+  for (int base = 0; base < count; base += kPlan) {
+    const int i = base + static_cast<int>(threadIdx.x);
+    const int want = i < count ? need(i) : 0;
+    mine |= want < 0;
+    uint64_t total;
+    const uint64_t before = carry + block_scan(static_cast<uint64_t>(max(want, 0)), total);
+    if (i < count) off[i] = static_cast<uint32_t>(min(before, static_cast<uint64_t>(0xFFFFFFFFu)));
+    carry += total;
+  }
+  bad = __syncthreads_or(mine);
+  return carry;
+}
+
+// Walks the free pages in ascending order until `want` of them have been seen; put(k, page)
+// for the k-th (k < want).  Returns how many were found.
+template <class Put>
+__device__ __forceinline__ uint32_t walk_free(const int32_t* ref, int n_pages, uint64_t want, Put put) {
+  uint32_t found = 0;
+  for (int base = 0; base < n_pages && found < want; base += kPlan * kScan) {
+    const int p0 = base + static_cast<int>(threadIdx.x) * kScan;
+    uint32_t bits = 0;
+#pragma unroll
+    for (int i = 0; i < kScan; ++i)
+      if (p0 + i < n_pages && ref[p0 + i] == 0) bits |= 1u << i;
+    uint32_t total;
+    uint32_t k = found + block_scan(static_cast<uint32_t>(__popc(bits)), total);
+#pragma unroll
+    for (int i = 0; i < kScan; ++i)
+      if ((bits >> i) & 1u) {
+        if (k < want) put(k, p0 + i);
+        ++k;
+      }
+    found += total;
+  }
+  return found;
+}
+
+// The taker whose requests cover page k: the last i with off[i] <= k (takers that ask
+// for none share their successor's offset).
+__device__ __forceinline__ int taker_of(const uint32_t* off, int count, uint32_t k) {
+  int lo = 0, hi = count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (off[mid] <= k)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Hands out the pages asked for, or none: 0, or the number missing.
+template <class Put>
+__device__ __forceinline__ int hand_out(const attn_kv_cache& c, uint64_t want, Put put) {
+  if (want == 0) return 0;
+  const uint64_t found = walk_free(c.ref_counts, c.n_pages, want, [](uint32_t, int) {});
+  if (found < want) return static_cast<int>(min(want - found, static_cast<uint64_t>(INT32_MAX)));
+  // a page is given away by the thread that reads its count, so the walk sees each once
+  walk_free(c.ref_counts, c.n_pages, want, [&](uint32_t k, int page) {
+    put(k, page);
+    c.ref_counts[page] = 1;
+  });
+  return 0;
+}
+
+__device__ __forceinline__ void report(int32_t* status, int value) {
+  if (threadIdx.x == 0) *status = value;
+}
+
+// ---------------------------------------------------------------------------- append
+__global__ void __launch_bounds__(kPlan) kv_append_plan_kernel(const attn_kv_cache c, int n_tokens,
+                                                               const int32_t* __restrict__ cu, int32_t* status) {
+  extern __shared__ uint32_t off[];
+  griddep_launch_dependents();
+  bool bad;
+  const uint64_t want = sum_requests(c.rows, off, bad, [&](int b) {
+    const int len = c.seq_lens[b], c0 = cu[b], c1 = cu[b + 1];
+    if (len < 0 || c0 < 0 || c1 < c0 || c1 > n_tokens) return -1;
+    const int64_t end = static_cast<int64_t>(len) + (c1 - c0);
+    if (end > static_cast<int64_t>(c.max_pages) * c.page_size) return -1;
+    return pages_of(static_cast<int>(end), c.page_size) - pages_of(len, c.page_size);
+  });
+  if (bad) return report(status, ATTN_KV_INVALID);
+  const int missing = hand_out(c, want, [&](uint32_t k, int page) {
+    const int b = taker_of(off, c.rows, k);
+    const int at = pages_of(c.seq_lens[b], c.page_size) + static_cast<int>(k - off[b]);
+    c.page_table[static_cast<int64_t>(b) * c.max_pages + at] = page;
+  });
+  __syncthreads();  // the lengths above have been read
+  if (missing == 0)
+    for (int b = threadIdx.x; b < c.rows; b += kPlan) c.seq_lens[b] += cu[b + 1] - cu[b];
+  report(status, missing);
+}
+
+// The row that token t belongs to (cu[b] <= t < cu[b + 1]), or -1; the warp's lanes probe 32
+// offsets at a time, so 1024 rows take two loads.
+__device__ __forceinline__ int row_of(const int32_t* cu, int rows, int t) {
+  if (t < cu[0] || t >= cu[rows]) return -1;
+  const int lane = static_cast<int>(threadIdx.x % 32);
+  int lo = 0, n = rows;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int i = lo + lane * step;
+    const bool below = lane * step < n && cu[i] <= t;
+    const int last = 31 - __clz(__ballot_sync(0xffffffffu, below));  // lane 0 always holds
+    lo += last * step;
+    n = min(step, n - last * step);
+  }
+  return lo;
+}
+
+struct NewTokens {
+  const __nv_bfloat16 *k, *v;
+  int64_t k_token, k_head, v_token, v_head;
+  int n;
+};
+
+// One warp per token: its K and V of every head, 16 bytes per lane and access, four of each in flight.
+template <int D>
+__global__ void __launch_bounds__(256) kv_append_write_kernel(const attn_kv_cache c, const NewTokens x,
+                                                              const int32_t* __restrict__ cu,
+                                                              const int32_t* status) {
+  constexpr int kChunks = D / 8;  // 16-byte chunks of a head's row
+  constexpr int kUnroll = 4;
+  griddep_wait();
+  if (*status != 0) return;
+  const int lane = threadIdx.x % 32;
+  const int per = c.Hkv * kChunks;
+  for (int t = (blockIdx.x * 256 + threadIdx.x) / 32; t < x.n; t += gridDim.x * 8) {
+    const int b = row_of(cu, c.rows, t);
+    if (b < 0) continue;
+    const int pos = c.seq_lens[b] - (cu[b + 1] - t);
+    const int page = c.page_table[static_cast<int64_t>(b) * c.max_pages + pos / c.page_size];
+    if (page < 0 || page >= c.n_pages) continue;
+    const int slot = pos % c.page_size;
+    const __nv_bfloat16* ks = x.k + t * x.k_token;
+    const __nv_bfloat16* vs = x.v + t * x.v_token;
+    __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(c.k) + page * c.k_stride_page + slot * c.k_stride_slot;
+    __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(c.v) + page * c.v_stride_page + slot * c.v_stride_slot;
+    for (int e0 = lane; e0 < per; e0 += 32 * kUnroll) {
+      uint4 kk[kUnroll], vv[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int e = e0 + 32 * u, h = e / kChunks, d = (e % kChunks) * 8;
+        if (e < per) {
+          kk[u] = *reinterpret_cast<const uint4*>(ks + h * x.k_head + d);
+          vv[u] = *reinterpret_cast<const uint4*>(vs + h * x.v_head + d);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int e = e0 + 32 * u, h = e / kChunks, d = (e % kChunks) * 8;
+        if (e < per) {
+          *reinterpret_cast<uint4*>(kd + h * c.k_stride_head + d) = kk[u];
+          *reinterpret_cast<uint4*>(vd + h * c.v_stride_head + d) = vv[u];
+        }
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------- fork
+// off: n offsets, then a bit per row.
+__global__ void __launch_bounds__(kPlan) kv_fork_plan_kernel(const attn_kv_cache c,
+                                                             const int32_t* __restrict__ parents,
+                                                             const int32_t* __restrict__ children, int n,
+                                                             int32_t* status) {
+  extern __shared__ uint32_t off[];
+  griddep_launch_dependents();
+  uint32_t* is_child = off + n;
+  const int words = (c.rows + 31) / 32;
+  for (int i = threadIdx.x; i < words; i += kPlan) is_child[i] = 0;
+  __syncthreads();
+  bool mine = false;
+  for (int i = threadIdx.x; i < n; i += kPlan) {
+    const int b = children[i];
+    if (b < 0 || b >= c.rows) {
+      mine = true;
+    } else {
+      mine |= c.seq_lens[b] != 0;
+      mine |= (atomicOr(&is_child[b / 32], 1u << (b % 32)) >> (b % 32)) & 1u;  // listed twice
+    }
+  }
+  if (__syncthreads_or(mine)) return report(status, ATTN_KV_INVALID);
+  bool bad;
+  const uint64_t want = sum_requests(n, off, bad, [&](int i) {
+    const int a = parents[i];
+    if (a < 0 || a >= c.rows || ((is_child[a / 32] >> (a % 32)) & 1u)) return -1;
+    const int len = c.seq_lens[a];
+    if (len < 0 || len > static_cast<int64_t>(c.max_pages) * c.page_size) return -1;
+    return len % c.page_size != 0 ? 1 : 0;
+  });
+  if (bad) return report(status, ATTN_KV_INVALID);
+  const int missing = hand_out(c, want, [&](uint32_t k, int page) {
+    const int i = taker_of(off, n, k);
+    c.page_table[static_cast<int64_t>(children[i]) * c.max_pages + c.seq_lens[parents[i]] / c.page_size] = page;
+  });
+  __syncthreads();
+  if (missing == 0)  // no child is a parent, so the lengths read are not those written
+    for (int i = threadIdx.x; i < n; i += kPlan) c.seq_lens[children[i]] = c.seq_lens[parents[i]];
+  report(status, missing);
+}
+
+// Block (i, 0): the child's table row and the counts of the pages it shares.  Block (i, 1 + h):
+// head h of the partly filled last page into the child's own.
+template <int D>
+__global__ void __launch_bounds__(256) kv_fork_move_kernel(const attn_kv_cache c,
+                                                           const int32_t* __restrict__ parents,
+                                                           const int32_t* __restrict__ children,
+                                                           const int32_t* status) {
+  constexpr int kChunks = D / 8;
+  griddep_wait();
+  if (*status != 0) return;
+  const int i = blockIdx.x;
+  const int a = parents[i], b = children[i];
+  const int len = c.seq_lens[a];
+  const int full = len / c.page_size, part = len % c.page_size;
+  int32_t* from = c.page_table + static_cast<int64_t>(a) * c.max_pages;
+  int32_t* to = c.page_table + static_cast<int64_t>(b) * c.max_pages;
+  if (blockIdx.y == 0) {
+    for (int p = threadIdx.x; p < c.max_pages; p += 256) {
+      if (p < full) {
+        const int page = from[p];
+        to[p] = page;
+        if (page >= 0 && page < c.n_pages) atomicAdd(&c.ref_counts[page], 1);
+      } else if (p > full || part == 0) {
+        to[p] = -1;
+      }
+    }
+    return;
+  }
+  if (part == 0) return;
+  const int src = from[full], dst = to[full];
+  if (src < 0 || src >= c.n_pages || dst < 0 || dst >= c.n_pages) return;
+  const int h = blockIdx.y - 1;
+  const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(c.k) + h * c.k_stride_head;
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(c.v) + h * c.v_stride_head;
+  __nv_bfloat16* kd = static_cast<__nv_bfloat16*>(c.k) + h * c.k_stride_head + dst * c.k_stride_page;
+  __nv_bfloat16* vd = static_cast<__nv_bfloat16*>(c.v) + h * c.v_stride_head + dst * c.v_stride_page;
+#pragma unroll 4
+  for (int e = threadIdx.x; e < part * kChunks; e += 256) {
+    const int slot = e / kChunks, d = (e % kChunks) * 8;
+    const uint4 kk = *reinterpret_cast<const uint4*>(k + src * c.k_stride_page + slot * c.k_stride_slot + d);
+    const uint4 vv = *reinterpret_cast<const uint4*>(v + src * c.v_stride_page + slot * c.v_stride_slot + d);
+    *reinterpret_cast<uint4*>(kd + slot * c.k_stride_slot + d) = kk;
+    *reinterpret_cast<uint4*>(vd + slot * c.v_stride_slot + d) = vv;
+  }
+}
+
+// ---------------------------------------------------------------------------- compact
+// One block per row.  Token i of the kept ones comes from place accepted[i] >= i, so
+// moving them in ascending order never overwrites a token that is still to move; a group
+// of tokens is read whole into registers before any of it is written.
+constexpr int kCompact = 512;  // threads
+constexpr int kHold = 4;       // 16-byte pieces of K and of V that a thread holds
+constexpr int kGroup = 128;    // tokens whose places are looked up at a time
+
+template <int D>
+__global__ void __launch_bounds__(kCompact) kv_compact_kernel(const attn_kv_cache c, const int32_t* __restrict__ cu,
+                                                              const int32_t* __restrict__ accepted, int n_accepted,
+                                                              const int32_t* __restrict__ cu_accepted,
+                                                              int32_t* __restrict__ status) {
+  constexpr int kChunks = D / 8;
+  __shared__ int2 s_from[kGroup], s_to[kGroup];  // page, slot
+  const int b = blockIdx.x, tid = threadIdx.x;
+  const int len = c.seq_lens[b];
+  const int n = cu[b + 1] - cu[b];
+  const int a0 = cu_accepted[b], a1 = cu_accepted[b + 1];
+  int32_t* table = c.page_table + static_cast<int64_t>(b) * c.max_pages;
+  const int ctx = len - n, m = a1 - a0;
+  // ---- the row's lists
+  bool bad = n < 0 || ctx < 0 || len > static_cast<int64_t>(c.max_pages) * c.page_size || a0 < 0 || m < 0 ||
+             a1 > n_accepted || m > n;
+  if (!bad) {
+    for (int i = tid; i < m; i += kCompact) {
+      const int x = accepted[a0 + i];
+      bad |= x < 0 || x >= n || (i > 0 && accepted[a0 + i - 1] >= x);
+      if (!bad && x != i) {  // it moves: its pages have to be there, the one it moves into its own
+        const int from = table[(ctx + x) / c.page_size], to = table[(ctx + i) / c.page_size];
+        bad |= from < 0 || from >= c.n_pages || to < 0 || to >= c.n_pages || c.ref_counts[to] != 1;
+      }
+    }
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) status[b] = bad ? ATTN_KV_INVALID : 0;
+  if (bad) return;
+  // ---- move
+  const int per = c.Hkv * kChunks;           // 16-byte pieces of one token's K (and of its V)
+  for (int g0 = 0; g0 < m; g0 += kGroup) {
+    const int cnt = min(kGroup, m - g0);
+    __syncthreads();
+    bool moves = false;
+    for (int i = tid; i < cnt; i += kCompact) {
+      const int x = accepted[a0 + g0 + i], src = ctx + x, dst = ctx + g0 + i;
+      s_from[i] = make_int2(table[src / c.page_size], src % c.page_size);
+      s_to[i] = make_int2(x == g0 + i ? -1 : table[dst / c.page_size], dst % c.page_size);
+      moves |= x != g0 + i;
+    }
+    if (!__syncthreads_or(moves)) continue;
+    const int pieces = cnt * per;
+    for (int e0 = 0; e0 < pieces; e0 += kCompact * kHold) {
+      uint4 kk[kHold], vv[kHold];
+#pragma unroll
+      for (int u = 0; u < kHold; ++u) {
+        const int e = e0 + u * kCompact + tid;
+        if (e >= pieces || s_to[e / per].x < 0) continue;
+        const int2 f = s_from[e / per];
+        const int h = (e % per) / kChunks, d = (e % kChunks) * 8;
+        kk[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.k) + f.x * c.k_stride_page +
+                                                h * c.k_stride_head + f.y * c.k_stride_slot + d);
+        vv[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(c.v) + f.x * c.v_stride_page +
+                                                h * c.v_stride_head + f.y * c.v_stride_slot + d);
+      }
+      __syncthreads();  // every read of the group is done
+#pragma unroll
+      for (int u = 0; u < kHold; ++u) {
+        const int e = e0 + u * kCompact + tid;
+        if (e >= pieces || s_to[e / per].x < 0) continue;
+        const int2 t = s_to[e / per];
+        const int h = (e % per) / kChunks, d = (e % kChunks) * 8;
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.k) + t.x * c.k_stride_page + h * c.k_stride_head +
+                                  t.y * c.k_stride_slot + d) = kk[u];
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(c.v) + t.x * c.v_stride_page + h * c.v_stride_head +
+                                  t.y * c.v_stride_slot + d) = vv[u];
+      }
+      __syncthreads();  // ... and written before the next one is read
+    }
+  }
+  // ---- the new length; pages past it
+  __syncthreads();
+  for (int p = pages_of(ctx + m, c.page_size) + tid; p < pages_of(len, c.page_size); p += kCompact) {
+    const int page = table[p];
+    if (page >= 0 && page < c.n_pages) atomicSub(&c.ref_counts[page], 1);
+    table[p] = -1;
+  }
+  if (tid == 0) c.seq_lens[b] = ctx + m;
+}
+
+// ---------------------------------------------------------------------------- free
+__global__ void __launch_bounds__(256) kv_free_kernel(const attn_kv_cache c, const int32_t* __restrict__ rows) {
+  __shared__ int s_len;
+  const int b = rows[blockIdx.x];
+  if (b < 0 || b >= c.rows) return;
+  if (threadIdx.x == 0) s_len = atomicExch(&c.seq_lens[b], 0);  // a row listed twice: the second finds 0
+  __syncthreads();
+  const int len = static_cast<int>(min(static_cast<int64_t>(max(s_len, 0)),
+                                       static_cast<int64_t>(c.max_pages) * c.page_size));
+  int32_t* table = c.page_table + static_cast<int64_t>(b) * c.max_pages;
+  for (int p = threadIdx.x; p < pages_of(len, c.page_size); p += 256) {
+    const int page = table[p];
+    if (page >= 0 && page < c.n_pages) atomicSub(&c.ref_counts[page], 1);
+    table[p] = -1;
+  }
+}
+
+// ----------------------------------------------------------------------------
+// host side
+// ----------------------------------------------------------------------------
+thread_local cudaError_t t_last_cuda_error = cudaSuccess;
+
+int cuda_fail(cudaError_t e) {
+  t_last_cuda_error = e;
+  return ATTN_ERR_CUDA;
+}
+
+int done(cudaError_t e) { return e == cudaSuccess ? ATTN_OK : cuda_fail(e); }
+
+// The device's multiprocessors, or a status.
+int device(int* sms) {
+  cudaError_t e;
+  const int n = attn_host::device_sms(&e);
+  if (n < 0) return cuda_fail(e);
+  *sms = n;
+  return n == 0 ? ATTN_ERR_UNSUPPORTED_DEVICE : ATTN_OK;
+}
+
+// Launch with programmatic stream serialisation: the kernel starts under the one before it
+// and waits for it with griddep_wait.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// The planning kernels keep a word per row or pair in shared memory, above 48 KB for many rows.
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  return bytes <= 48 * 1024 ? cudaSuccess
+                            : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   static_cast<int>(bytes));
+}
+
+}  // namespace
+
+extern "C" {
+
+int attn_kv_append(const attn_kv_cache* cache, const void* k_new, const void* v_new, int64_t k_stride_token,
+                   int64_t k_stride_head, int64_t v_stride_token, int64_t v_stride_head, int n_tokens,
+                   const int32_t* cu_tokens, int32_t* status, cudaStream_t stream) {
+  int st = attn_host::check_cache(cache, true, true);
+  if (st != ATTN_OK) return st;
+  if (n_tokens < 0) return ATTN_ERR_INVALID_ARG;
+  if (!cu_tokens || !status) return ATTN_ERR_NULL_PTR;
+  if (!attn_host::aligned_to(cu_tokens, 4) || !attn_host::aligned_to(status, 4)) return ATTN_ERR_MISALIGNED;
+  if (n_tokens > 0) {
+    if (!k_new || !v_new) return ATTN_ERR_NULL_PTR;
+    if (!attn_host::aligned_to(k_new, 16) || !attn_host::aligned_to(v_new, 16)) return ATTN_ERR_MISALIGNED;
+    const int64_t strides[] = {k_stride_token, k_stride_head, v_stride_token, v_stride_head};
+    for (int64_t s : strides)
+      if (s < 0 || s % 8 != 0) return ATTN_ERR_INVALID_ARG;
+    if (cache->k == cache->v && cache->n_pages > 0) return ATTN_ERR_INVALID_ARG;
+  }
+  int sms = 0;
+  st = device(&sms);
+  if (st != ATTN_OK) return st;
+  const size_t smem = static_cast<size_t>(cache->rows + 1) * 4;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kv_append_plan_kernel), smem);
+  if (e != cudaSuccess) return cuda_fail(e);
+  kv_append_plan_kernel<<<1, kPlan, smem, stream>>>(*cache, n_tokens, cu_tokens, status);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (n_tokens == 0 || cache->rows == 0 || cache->n_pages == 0) return ATTN_OK;
+  const NewTokens x{static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new),
+                    k_stride_token, k_stride_head, v_stride_token, v_stride_head, n_tokens};
+  const int blocks = std::min((n_tokens + 7) / 8, sms * 8);
+  return done(cache->D == 128
+                  ? launch_after(kv_append_write_kernel<128>, dim3(blocks), 256, stream, *cache, x, cu_tokens, status)
+                  : launch_after(kv_append_write_kernel<64>, dim3(blocks), 256, stream, *cache, x, cu_tokens, status));
+}
+
+int attn_kv_fork(const attn_kv_cache* cache, const int32_t* parents, const int32_t* children, int n, int32_t* status,
+                 cudaStream_t stream) {
+  int st = attn_host::check_cache(cache, true, true);
+  if (st != ATTN_OK) return st;
+  // a child is listed once, so more pairs than rows never fit
+  if (n < 0 || n > cache->rows || cache->Hkv > 65534) return ATTN_ERR_INVALID_ARG;
+  if (!status || (n > 0 && (!parents || !children))) return ATTN_ERR_NULL_PTR;
+  if (!attn_host::aligned_to(parents, 4) || !attn_host::aligned_to(children, 4) || !attn_host::aligned_to(status, 4))
+    return ATTN_ERR_MISALIGNED;
+  int sms = 0;
+  st = device(&sms);
+  if (st != ATTN_OK) return st;
+  const size_t smem = (static_cast<size_t>(n) + (cache->rows + 31) / 32 + 1) * 4;
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kv_fork_plan_kernel), smem);
+  if (e != cudaSuccess) return cuda_fail(e);
+  kv_fork_plan_kernel<<<1, kPlan, smem, stream>>>(*cache, parents, children, n, status);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (n == 0) return ATTN_OK;
+  const dim3 grid(n, 1 + cache->Hkv);
+  return done(cache->D == 128
+                  ? launch_after(kv_fork_move_kernel<128>, grid, 256, stream, *cache, parents, children, status)
+                  : launch_after(kv_fork_move_kernel<64>, grid, 256, stream, *cache, parents, children, status));
+}
+
+int attn_kv_compact(const attn_kv_cache* cache, const int32_t* cu_tokens, const int32_t* accepted, int n_accepted,
+                    const int32_t* cu_accepted, int32_t* status, cudaStream_t stream) {
+  int st = attn_host::check_cache(cache, true, true);
+  if (st != ATTN_OK) return st;
+  if (n_accepted < 0) return ATTN_ERR_INVALID_ARG;
+  if (cache->rows == 0) return ATTN_OK;
+  if (!cu_tokens || !cu_accepted || !status || (n_accepted > 0 && !accepted)) return ATTN_ERR_NULL_PTR;
+  if (!attn_host::aligned_to(cu_tokens, 4) || !attn_host::aligned_to(accepted, 4) ||
+      !attn_host::aligned_to(cu_accepted, 4) || !attn_host::aligned_to(status, 4))
+    return ATTN_ERR_MISALIGNED;
+  int sms = 0;
+  st = device(&sms);
+  if (st != ATTN_OK) return st;
+  if (cache->D == 128)
+    kv_compact_kernel<128><<<cache->rows, kCompact, 0, stream>>>(*cache, cu_tokens, accepted, n_accepted, cu_accepted,
+                                                                 status);
+  else
+    kv_compact_kernel<64><<<cache->rows, kCompact, 0, stream>>>(*cache, cu_tokens, accepted, n_accepted, cu_accepted,
+                                                                status);
+  return done(cudaGetLastError());
+}
+
+int attn_kv_free(const attn_kv_cache* cache, const int32_t* rows, int n, cudaStream_t stream) {
+  int st = attn_host::check_cache(cache, false, true);
+  if (st != ATTN_OK) return st;
+  if (n < 0) return ATTN_ERR_INVALID_ARG;
+  if (n == 0 || cache->rows == 0) return ATTN_OK;
+  if (!rows) return ATTN_ERR_NULL_PTR;
+  if (!attn_host::aligned_to(rows, 4)) return ATTN_ERR_MISALIGNED;
+  int sms = 0;
+  st = device(&sms);
+  if (st != ATTN_OK) return st;
+  kv_free_kernel<<<n, 256, 0, stream>>>(*cache, rows);
+  return done(cudaGetLastError());
+}
+
+const char* attn_kv_strerror(int status) { return attn_host::status_text(status, t_last_cuda_error); }
+
+}  // extern "C"

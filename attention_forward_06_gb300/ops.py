@@ -10,7 +10,7 @@ import math
 
 import torch
 
-from ._lib import load
+from ._lib import KvCache, load
 
 ATTN_OK = 0
 ATTN_ERR_INVALID_ARG = 1
@@ -377,6 +377,124 @@ def attn_bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
     if st != ATTN_OK:
         raise AttnError(st, lib.attn_bwd_strerror(st).decode())
     return dq, dk, dv
+
+
+KV_INVALID = -1  # device status: lengths, indices or lists that do not fit each other (ATTN_KV_INVALID)
+
+
+def _int32(name: str, t: torch.Tensor, *shape) -> torch.Tensor:
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or \
+            any(n is not None and t.shape[i] != n for i, n in enumerate(shape)):
+        want = ", ".join("n" if n is None else str(n) for n in shape)
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{want}]")
+    return t
+
+
+def _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts=None) -> KvCache:
+    """The C ABI's cache of ``k_pages``/``v_pages [pages, Hkv, page_size, D]`` (any strides but the last, 1)."""
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
+            raise ValueError(f"{name} must be a 4-d bf16 tensor [pages, Hkv, page_size, D] whose last stride is 1")
+    if v_pages.shape != k_pages.shape:
+        raise ValueError(f"shape mismatch k_pages{tuple(k_pages.shape)} v_pages{tuple(v_pages.shape)}")
+    n_pages, Hkv, page_size, D = k_pages.shape
+    rows, max_pages = _int32("page_table", page_table, None, None).shape
+    _int32("seq_lens", seq_lens, rows)
+    if ref_counts is not None:
+        _int32("ref_counts", ref_counts, n_pages)
+    return KvCache(k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.stride()[:3], *v_pages.stride()[:3],
+                   page_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr() if ref_counts is not None else None,
+                   n_pages, Hkv, page_size, D, rows, max_pages)
+
+
+def _check_kv(status: int) -> None:
+    if status != ATTN_OK:
+        raise AttnError(status, load("attn_kv").attn_kv_strerror(status).decode())
+
+
+def _status(status, n: int, device) -> torch.Tensor:
+    return torch.empty(n, dtype=torch.int32, device=device) if status is None else _int32("status", status, n)
+
+
+def kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+              page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, cu_tokens: torch.Tensor,
+              status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Append tokens to a paged cache; returns the device ``status [1]``.
+
+    Row b's tokens ``[cu_tokens[b], cu_tokens[b+1])`` of ``k_new``/``v_new [tokens, Hkv, D]`` (bf16, last stride 1) go
+    behind its ``seq_lens[b]`` tokens, which grow; pages are taken as they are needed.  ``status`` is 0, the number
+    of pages missing, or ``KV_INVALID``; unless it is 0 nothing has changed.  Nothing waits for the device.
+    """
+    dev = _on_device(k_pages=k_pages, v_pages=v_pages, k_new=k_new, v_new=v_new, page_table=page_table,
+                     seq_lens=seq_lens, ref_counts=ref_counts, cu_tokens=cu_tokens, status=status)
+    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (cache.Hkv, cache.D) or t.stride(2) != 1:
+            raise ValueError(f"{name} must be a bf16 tensor [tokens, {cache.Hkv}, {cache.D}] whose last stride is 1")
+    if v_new.shape != k_new.shape:
+        raise ValueError(f"shape mismatch k_new{tuple(k_new.shape)} v_new{tuple(v_new.shape)}")
+    _int32("cu_tokens", cu_tokens, cache.rows + 1)
+    status = _status(status, 1, dev)
+    _check_kv(load("attn_kv").attn_kv_append(cache, k_new.data_ptr(), v_new.data_ptr(), *k_new.stride()[:2],
+                                             *v_new.stride()[:2], k_new.shape[0], cu_tokens.data_ptr(),
+                                             status.data_ptr(), _stream_handle(stream)))
+    return status
+
+
+def kv_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+            ref_counts: torch.Tensor, parents: torch.Tensor, children: torch.Tensor,
+            status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Make each empty row ``children[i]`` a copy of row ``parents[i]``; returns the device ``status [1]``.
+
+    Full pages are shared, a partly filled last page is copied.  ``status`` as ``kv_append``'s.
+    """
+    dev = _on_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
+                     ref_counts=ref_counts, parents=parents, children=children, status=status)
+    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
+    n = _int32("parents", parents, None).shape[0]
+    _int32("children", children, n)
+    status = _status(status, 1, dev)
+    _check_kv(load("attn_kv").attn_kv_fork(cache, parents.data_ptr(), children.data_ptr(), n, status.data_ptr(),
+                                           _stream_handle(stream)))
+    return status
+
+
+def kv_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+               ref_counts: torch.Tensor, cu_tokens: torch.Tensor, accepted: torch.Tensor, cu_accepted: torch.Tensor,
+               status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Keep the accepted ones of each row's newest tokens; returns the device ``status [rows]``.
+
+    Of row b's ``cu_tokens[b+1] - cu_tokens[b]`` newest tokens, those that ``accepted[cu_accepted[b] :
+    cu_accepted[b+1]]`` lists (ascending) move together, the others are dropped and pages past the end are given
+    back.  ``status[b]`` is 0, or ``KV_INVALID`` for a row that is left as it was.
+    """
+    dev = _on_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
+                     ref_counts=ref_counts, cu_tokens=cu_tokens, accepted=accepted, cu_accepted=cu_accepted,
+                     status=status)
+    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
+    _int32("cu_tokens", cu_tokens, cache.rows + 1)
+    _int32("cu_accepted", cu_accepted, cache.rows + 1)
+    _int32("accepted", accepted, None)
+    status = _status(status, cache.rows, dev)
+    _check_kv(load("attn_kv").attn_kv_compact(cache, cu_tokens.data_ptr(), accepted.data_ptr(), accepted.shape[0],
+                                              cu_accepted.data_ptr(), status.data_ptr(), _stream_handle(stream)))
+    return status
+
+
+def kv_free(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
+            page_size: int, stream=None) -> None:
+    """Free the rows listed: their pages' counts fall, their table entries become -1, their lengths 0.
+
+    A row listed twice is freed once; one that is out of range is passed over.
+    """
+    _on_device(page_table=page_table, seq_lens=seq_lens, ref_counts=ref_counts, rows=rows)
+    n_rows, max_pages = _int32("page_table", page_table, None, None).shape
+    _int32("seq_lens", seq_lens, n_rows)
+    n_pages = _int32("ref_counts", ref_counts, None).shape[0]
+    n = _int32("rows", rows, None).shape[0]
+    cache = KvCache(page_table=page_table.data_ptr(), seq_lens=seq_lens.data_ptr(), ref_counts=ref_counts.data_ptr(),
+                    n_pages=n_pages, Hkv=1, page_size=int(page_size), D=64, rows=n_rows, max_pages=max_pages)
+    _check_kv(load("attn_kv").attn_kv_free(cache, rows.data_ptr(), n, _stream_handle(stream)))
 
 
 def bwd_debug_status(stream=None) -> tuple[int, int]:

@@ -1,0 +1,120 @@
+/*
+ * attn_kv.h -- C ABI of a paged key/value cache for GB300 (sm_103a): its layout, and
+ * the calls that append tokens to it, fork sequences, keep the accepted ones of
+ * drafted tokens, and free sequences.  attn_fwd_tree (attn_paged.h) is the attention
+ * that reads it.  Everything a call needs (page table, lengths, reference counts)
+ * lies in device memory and is changed there, so a serving step enqueues its
+ * calls without waiting for the device, and can be captured into a CUDA graph.
+ *
+ * Layout.  A cache is a pool of pages, each holding `page_size` tokens of every kv
+ * head, and rows (sequences) that list their pages:
+ *     k, v        bf16, element (page, head, slot, d) at
+ *                 page * stride_page + head * stride_head + slot * stride_slot + d
+ *                 (strides in elements, multiples of 8; the places of different
+ *                 elements must differ, K and V may be interleaved)
+ *     page_table  int32 [rows][max_pages]: token t of row b is in slot t % page_size of
+ *                 page page_table[b][t / page_size]; entries past the row's pages are
+ *                 not read
+ *     seq_lens    int32 [rows]: tokens of each row, the newest (drafted) ones included
+ *     ref_counts  int32 [n_pages]: rows that list the page; 0 is a free page
+ * D is 64 or 128; page_size 16, 32, 64, 128 or 256; rows at most 32768; n_pages at most
+ * 4000000; k, v 16-byte aligned, the int32 arrays 4-byte aligned.
+ *
+ * A call that takes pages takes the free pages with the lowest numbers, in the order
+ * of the rows (or pairs) and of their tokens, so equal states and calls give equal
+ * page tables.
+ *
+ * Every call is asynchronous on `stream`, allocates nothing, and checks on the host
+ * what the host knows (attn_fwd.h's status codes).  What only the device knows it
+ * checks there: it then changes nothing and reports in `status` (device memory).
+ * Calls on one cache must be ordered (one stream, or events); calls on different
+ * caches may overlap.
+ */
+#ifndef ATTN_KV_H
+#define ATTN_KV_H
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "attn_fwd.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define ATTN_KV_MAX_ROWS 32768
+#define ATTN_KV_MAX_PAGES 4000000
+
+/* Device status words: 0 done, a positive number the pages that were missing, or */
+#define ATTN_KV_INVALID (-1) /* lengths, indices or lists that do not fit each other */
+
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_stride_page, k_stride_head, k_stride_slot;
+  int64_t v_stride_page, v_stride_head, v_stride_slot;
+  int32_t* page_table;
+  int32_t* seq_lens;
+  int32_t* ref_counts; /* not used by attn_fwd_tree */
+  int32_t n_pages, Hkv, page_size, D;
+  int32_t rows, max_pages;
+} attn_kv_cache;
+
+/*
+ * Append tokens: row b's tokens [cu_tokens[b], cu_tokens[b + 1]) of k_new, v_new go
+ * behind its seq_lens[b] tokens, pages are taken where the last one is full, and
+ * seq_lens[b] grows.  k_new, v_new: bf16, element (token, head, d) at token *
+ * stride_token + head * stride_head + d (multiples of 8, 16-byte aligned), n_tokens
+ * tokens; those in no row's range are ignored.  cu_tokens: int32 [rows + 1].
+ * status: int32 [1], written: 0; the number of pages missing; or ATTN_KV_INVALID
+ * (cu_tokens falls or leaves [0, n_tokens], a length is negative, a row would pass
+ * max_pages).  Unless it is 0 nothing has changed.  A row's last page must not be
+ * shared while it is partly filled (attn_kv_fork leaves none).
+ */
+int attn_kv_append(const attn_kv_cache* cache, const void* k_new, const void* v_new, int64_t k_stride_token,
+                   int64_t k_stride_head, int64_t v_stride_token, int64_t v_stride_head, int n_tokens,
+                   const int32_t* cu_tokens, int32_t* status, cudaStream_t stream);
+
+/*
+ * Fork: for each of n pairs, the empty row children[i] becomes a copy of row
+ * parents[i].  Full pages are shared (their counts grow); a partly filled last page is
+ * copied into a page of the child's own, so both may be appended to.  A parent may
+ * have several children.  The child's table entries past its pages become -1.
+ * status: int32 [1], written: 0; the number of pages missing; or ATTN_KV_INVALID (an
+ * index out of range, a child that is not empty, is listed twice or is a parent
+ * too).  Unless it is 0 nothing has changed.
+ */
+int attn_kv_fork(const attn_kv_cache* cache, const int32_t* parents, const int32_t* children, int n, int32_t* status,
+                 cudaStream_t stream);
+
+/*
+ * Keep the accepted ones of each row's newest tokens: of the n_b =
+ * cu_tokens[b + 1] - cu_tokens[b] newest tokens of row b, those that accepted[
+ * cu_accepted[b] .. cu_accepted[b + 1]) lists (ascending, in [0, n_b)) move together
+ * behind the tokens before them, the others are dropped, and pages past the end are
+ * given back (their table entries become -1).  With an empty list all n_b are
+ * dropped.  accepted holds n_accepted entries.
+ * status: int32 [rows], written: 0, or ATTN_KV_INVALID for a row that is left as it
+ * was: offsets that fall or leave their arrays, a list that is not ascending or out of range,
+ * n_b over the row's length, or a page that tokens would move into and another row shares.
+ */
+int attn_kv_compact(const attn_kv_cache* cache, const int32_t* cu_tokens, const int32_t* accepted, int n_accepted,
+                    const int32_t* cu_accepted, int32_t* status, cudaStream_t stream);
+
+/*
+ * Free the n rows listed: their pages' counts fall, their table entries become -1 and
+ * their lengths 0.  A row listed twice is freed once; one out of range is passed
+ * over.  k and v are not used and may be NULL.
+ */
+int attn_kv_free(const attn_kv_cache* cache, const int32_t* rows, int n, cudaStream_t stream);
+
+/* Text for a status code (ATTN_ERR_CUDA names this library's last CUDA error on the
+   calling thread). */
+const char* attn_kv_strerror(int status);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* ATTN_KV_H */

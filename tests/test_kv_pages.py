@@ -1,0 +1,358 @@
+"""The calls on a paged key/value cache (kv_append, kv_fork, kv_compact, kv_free) against plain loops on the host.
+Rows are moved and counted, so everything is compared bit for bit: K and V, the page table, lengths and counts."""
+import ctypes
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+from attention_forward_06_gb300 import _lib, ops
+from attention_forward_06_gb300 import build as B
+from paged_model import Model, empty_cache, i32, pool, same
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+gpu = pytest.mark.gpu
+
+
+def new_tokens(n, Hkv, D, seed):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn((n, Hkv, D), generator=g).to(torch.bfloat16).cuda() for _ in "kv"]
+
+
+def append(cache, model, n, seed=1, slack=0):
+    cu = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
+    k, v = new_tokens(int(cu[-1]) + slack, cache[0].shape[1], cache[0].shape[3], seed)
+    got = ops.kv_append(k, v, *cache, i32(cu)).item()
+    want = model.append(k, v, cu)
+    assert got == want
+    return got
+
+
+def fork(cache, model, parents, children):
+    got = ops.kv_fork(*cache, i32(parents), i32(children)).item()
+    want = model.fork(list(parents), list(children))
+    assert got == want
+    return got
+
+
+def compact(cache, model, n, accepted):
+    cu = np.concatenate([[0], np.cumsum(n)])
+    cu_acc = np.concatenate([[0], np.cumsum([len(a) for a in accepted])])
+    flat = np.concatenate([np.asarray(a, np.int64) for a in accepted]) if len(accepted) else np.zeros(0, np.int64)
+    got = ops.kv_compact(*cache, i32(cu), i32(flat), i32(cu_acc)).cpu().numpy()
+    want = model.compact(cu, flat, cu_acc)
+    assert np.array_equal(got, want)
+    return got
+
+
+def free(cache, model, rows):
+    ops.kv_free(*cache[2:], i32(rows), cache[0].shape[2])
+    model.free([b for i, b in enumerate(rows) if b not in rows[:i]])
+
+
+@gpu
+@pytest.mark.parametrize("P,D,Hkv,layout", [(16, 128, 8, "heads"), (32, 64, 3, "slots"), (64, 128, 1, "pairs"),
+                                            (128, 64, 5, "heads"), (256, 128, 2, "slots")])
+def test_a_random_program_of_calls(P, D, Hkv, layout):
+    rng = np.random.default_rng(P + D)
+    rows, max_pages = 9, 5
+    cache = empty_cache(rows * max_pages - 6, Hkv, P, D, rows, max_pages, layout, seed=P)
+    model = Model(*cache)
+    for step in range(40):
+        do = rng.integers(0, 4)
+        if do == 0:
+            append(cache, model, rng.integers(0, P + 3, rows) * rng.integers(0, 2, rows), seed=step, slack=step % 3)
+        elif do == 1:
+            empty = [b for b in range(rows) if model.lens[b] == 0]
+            full = [b for b in range(rows) if model.lens[b]]
+            if empty and full:
+                kids = rng.permutation(empty)[:rng.integers(1, len(empty) + 1)]
+                fork(cache, model, rng.choice(full, len(kids)), kids)
+        elif do == 2:
+            n = np.minimum(model.lens, rng.integers(0, P, rows))
+            acc = [np.sort(rng.permutation(m)[:rng.integers(0, m + 1)]) for m in n]
+            compact(cache, model, n, acc)
+        else:
+            free(cache, model, rng.integers(-1, rows + 1, 2).tolist())
+        same(model, cache)
+
+
+@gpu
+def test_a_row_stays_usable_through_the_pages_edges():
+    P = 16
+    cache = empty_cache(20, 2, P, 64, 3, 6)
+    model = Model(*cache)
+    for n in ([0, 1, P], [P - 1, P - 1, 1], [1, 0, 0], [1, 1, 2 * P], [0, 0, 0]):
+        assert append(cache, model, np.array(n), seed=sum(n)) == 0
+        same(model, cache)
+    assert compact(cache, model, np.array([2, 0, P]), [[1], [], []]).tolist() == [0, 0, 0]
+    same(model, cache)
+    assert compact(cache, model, np.array([1, 1, 1]), [[0], [0], [0]]).tolist() == [0, 0, 0]  # nothing moves
+    same(model, cache)
+
+
+@gpu
+def test_a_shortage_changes_nothing_and_says_how_much():
+    cache = empty_cache(4, 2, 16, 64, 3, 8)
+    model = Model(*cache)
+    assert append(cache, model, np.array([16, 16, 1])) == 0
+    before = [t.clone() for t in cache]
+    assert append(cache, model, np.array([32, 16, 15])) == 2  # three more pages, one is left
+    assert fork(cache, model, [2], [0]) == ops.KV_INVALID     # not empty
+    assert all(torch.equal(a, b) for a, b in zip(before, cache))
+    free(cache, model, [0])
+    assert append(cache, model, np.array([0, 30, 0])) == 0    # two more pages, then none
+    before = [t.clone() for t in cache]
+    assert fork(cache, model, [2], [0]) == 1
+    assert all(torch.equal(a, b) for a, b in zip(before, cache))
+
+
+@gpu
+def test_lists_that_do_not_fit_change_nothing():
+    cache = empty_cache(16, 2, 16, 64, 4, 3)
+    model = Model(*cache)
+    append(cache, model, np.array([20, 0, 0, 7]))
+    before = [t.clone() for t in cache]
+    unchanged = lambda: all(torch.equal(a, b) for a, b in zip(before, cache))  # noqa: E731
+    k, v = new_tokens(8, 2, 64, 3)
+    for cu in ([0, 2, 1, 3, 3], [0, 1, 2, 3, 9], [-1, 1, 2, 3, 4], [5, 4, 4, 4, 4]):
+        assert ops.kv_append(k, v, *cache, i32(cu)).item() == ops.KV_INVALID
+    k, v = new_tokens(40, 2, 64, 3)
+    assert ops.kv_append(k, v, *cache, i32([0, 29, 29, 29, 29])).item() == ops.KV_INVALID  # past max_pages
+    for parents, children in (([0, 3], [1, 1]), ([0, 1], [1, 2]), ([0], [3]), ([0], [4]), ([4], [1]), ([-1], [1]),
+                              ([0], [-1]), ([1], [1])):
+        assert ops.kv_fork(*cache, i32(parents), i32(children)).item() == ops.KV_INVALID, (parents, children)
+    assert unchanged()
+    # a bad list leaves its own row as it was, and only that row
+    n, cu = [6, 0, 0, 5], i32([0, 6, 6, 6, 11])
+    for acc in ([2, 1], [1, 1], [-1], [6], [0, 1, 2, 3, 4, 5, 5]):
+        flat, ends = i32(acc + [0]), i32([0, len(acc), len(acc), len(acc), len(acc) + 1])
+        assert ops.kv_compact(*cache, cu, flat, ends).tolist() == [-1, 0, 0, 0]
+        model.drop(3, 3)
+        same(model, cache)
+        append(cache, model, np.array([0, 0, 0, 4]))
+    for ends in ([0, -1, 0, 0, 0], [1, 0, 0, 0, 0], [0, 2, 2, 2, 2]):
+        assert ops.kv_compact(*cache, cu, i32([0]), i32(ends)).tolist()[0] == -1
+    assert ops.kv_compact(*cache, i32([0, 21, 21, 21, 21]), i32([0]), i32([0, 1, 1, 1, 1])).tolist()[0] == -1
+
+
+@gpu
+def test_shared_pages_are_not_moved_into():
+    cache = empty_cache(16, 2, 16, 64, 3, 4)
+    model = Model(*cache)
+    append(cache, model, np.array([40, 0, 0]))
+    assert fork(cache, model, [0], [1]) == 0
+    # tokens 30 and 31 of row 0 lie in a page that row 1 lists too: moving 31 to 30 is refused, dropping is not
+    assert compact(cache, model, np.array([10, 0, 0]), [[1], [], []]).tolist() == [-1, 0, 0]
+    same(model, cache)
+    assert compact(cache, model, np.array([20, 20, 0]), [[], [0, 1], []]).tolist() == [0, 0, 0]
+    same(model, cache)
+
+
+@gpu
+def test_freeing_twice_and_out_of_range():
+    cache = empty_cache(8, 1, 16, 64, 3, 2)
+    model = Model(*cache)
+    append(cache, model, np.array([17, 3, 32]))
+    free(cache, model, [2, 0, 2, -1, 3, 2 ** 31 - 1, 0])
+    same(model, cache)
+    free(cache, model, [2])
+    same(model, cache)
+
+
+@gpu
+def test_many_rows_and_pages():
+    # more rows than a planning block's threads and its 48 KB, more pages than one step of the walk
+    rows, P = 20000, 16
+    cache = empty_cache(33000, 1, P, 64, rows, 2, seed=5)
+    rng = np.random.default_rng(5)
+    n = rng.integers(0, 18, rows)
+    model = Model(*cache)
+    assert append(cache, model, n) == 0
+    same(model, cache)
+    free(cache, model, rng.permutation(rows)[:9000].tolist())
+    same(model, cache)
+    empty, full = np.flatnonzero(model.lens == 0), np.flatnonzero(model.lens)
+    assert fork(cache, model, rng.choice(full, 5000), rng.permutation(empty)[:5000]) == 0
+    same(model, cache)
+
+
+@gpu
+def test_long_moves():
+    # more accepted tokens than one look-up group, more pieces than the block holds at once
+    P, n = 32, 700
+    cache = empty_cache(60, 8, P, 128, 2, 25, seed=6)
+    model = Model(*cache)
+    append(cache, model, np.array([19, 5]))
+    append(cache, model, np.array([n, n - 11]))
+    rng = np.random.default_rng(6)
+    acc = [np.sort(rng.permutation(m)[:m // 2]) for m in (n, n - 11)]
+    assert compact(cache, model, np.array([n, n - 11]), acc).tolist() == [0, 0]
+    same(model, cache)
+
+
+@gpu
+def test_new_tokens_as_a_slice_of_a_fused_projection():
+    cache = empty_cache(8, 2, 16, 64, 2, 4)
+    model = Model(*cache)
+    fused = torch.randn((9, 8 * 64), generator=torch.Generator().manual_seed(2)).to(torch.bfloat16).cuda()
+    k, v = fused[:, 256:384].view(9, 2, 64), fused[:, 384:].view(9, 2, 64)
+    cu = np.array([2, 5, 8])  # tokens 0, 1 and 8 belong to no row
+    assert ops.kv_append(k, v, *cache, i32(cu)).item() == 0
+    model.append(k, v, cu)
+    same(model, cache)
+
+
+@gpu
+def test_in_a_graph_with_another_cache_on_another_stream():
+    def steps(cache, kv, status):
+        ops.kv_fork(*cache, i[0], i[1], status=status[:1])
+        ops.kv_append(*kv, *cache, i[2], status=status[1:2])
+        ops.kv_compact(*cache, i[2], i[3], i[4], status=status[2:])
+        ops.kv_free(*cache[2:], i[1], 16)
+
+    i = [i32([0, 0]), i32([1, 2]), i32([0, 0, 5, 9]), i32([1, 3, 2]), i32([0, 0, 2, 3])]
+    caches, models = [], []
+    for seed in (1, 2):
+        caches.append(empty_cache(12, 2, 16, 64, 3, 3, seed=seed))
+        models.append(Model(*caches[-1]))
+        append(caches[-1], models[-1], np.array([21, 0, 0]), seed=seed)
+    kv = [new_tokens(9, 2, 64, s) for s in (3, 4)]
+    status = [torch.full((5,), 7, dtype=torch.int32, device="cuda") for _ in range(2)]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        steps(caches[0], kv[0], status[0])
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graph.replay()
+        with torch.cuda.stream(side):
+            steps(caches[1], kv[1], status[1])
+    torch.cuda.synchronize()
+    for c in range(2):
+        for _ in range(3):
+            assert models[c].fork([0, 0], [1, 2]) == 0
+            assert models[c].append(*kv[c], np.array([0, 0, 5, 9])) == 0
+            assert not models[c].compact([0, 0, 5, 9], [1, 3, 2], [0, 0, 2, 3]).any()
+            models[c].free([1, 2])
+        same(models[c], caches[c])
+        assert not status[c].any()
+
+
+@gpu
+def test_nothing_to_do():
+    cache = empty_cache(4, 2, 16, 64, 2, 2)
+    model = Model(*cache)
+    none = i32([])
+    assert ops.kv_fork(*cache, none, none).item() == 0
+    ops.kv_free(*cache[2:], none, 16)
+    assert append(cache, model, np.array([0, 0])) == 0
+    assert compact(cache, model, np.array([0, 0]), [[], []]).tolist() == [0, 0]
+    same(model, cache)
+
+
+@gpu
+def test_offsets_past_32_bits():
+    # a pool of more than 2^31 elements: the last pages are taken, written, copied and moved within
+    n_pages, Hkv, P, D = 16500, 8, 128, 128
+    assert n_pages * Hkv * P * D > 2 ** 31
+    if torch.cuda.mem_get_info()[0] < (16 << 30):
+        pytest.skip("needs 16 GB of free device memory")
+    k = torch.zeros((n_pages, Hkv, P, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    ref = torch.ones(n_pages, dtype=torch.int32, device="cuda")
+    ref[-2:] = 0
+    table, lens = torch.full((2, 2), -1, dtype=torch.int32, device="cuda"), i32([0, 0])
+    kn, vn = new_tokens(9, Hkv, D, 1)
+    assert ops.kv_append(kn, vn, k, v, table, lens, ref, i32([0, 9, 9])).item() == 0
+    assert ops.kv_fork(k, v, table, lens, ref, i32([0]), i32([1])).item() == 0
+    assert ops.kv_compact(k, v, table, lens, ref, i32([0, 9, 9]), i32([3, 8]), i32([0, 2, 2])).tolist() == [0, 0]
+    assert table.tolist() == [[n_pages - 2, -1], [n_pages - 1, -1]] and lens.tolist() == [2, 9]
+    for pool_, new in ((k, kn), (v, vn)):
+        assert torch.equal(pool_[-2, :, :2], new[[3, 8]].transpose(0, 1))
+        assert torch.equal(pool_[-1, :, :9], new.transpose(0, 1))
+        assert not pool_[:-2].any()
+
+
+# ---------------------------------------------------------------------------- on the CPU
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return _lib.load("attn_kv")
+
+
+def test_exports_what_the_header_declares(lib):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include/attn_kv.h")).read(), flags=re.S)
+    funcs = set(re.findall(r"^\s*(?:const\s+)?\w+\s*\*?\s*(attn_kv_\w+)\s*\(", text, flags=re.M))
+    assert funcs == set(_lib.SIGNATURES["attn_kv"]) and len(funcs) == 5
+    assert all(hasattr(lib, f) for f in funcs)
+
+
+def fake(**kw):
+    """A cache at addresses that are never read: the host's checks come first."""
+    a = dict(k=0x1000000, v=0x2000000, k_stride_page=2 * 16 * 64, k_stride_head=16 * 64, k_stride_slot=64,
+             v_stride_page=2 * 16 * 64, v_stride_head=16 * 64, v_stride_slot=64, page_table=0x3000000,
+             seq_lens=0x3100000, ref_counts=0x3200000, n_pages=10, Hkv=2, page_size=16, D=64, rows=4, max_pages=5)
+    return _lib.KvCache(**dict(a, **kw))
+
+
+def call_append(lib, cache, k=0x4000000, n=4, cu=0x5000000, status=0x5100000, stride=128):
+    return lib.attn_kv_append(cache, k, 0x4100000, stride, 64, 128, 64, n, cu, status, None)
+
+
+BAD_CACHES = [
+    dict(D=96), dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(Hkv=0), dict(rows=-1),
+    dict(rows=32769), dict(n_pages=4000001), dict(n_pages=-1), dict(max_pages=-1), dict(max_pages=2 ** 28),
+    dict(k_stride_slot=0), dict(k_stride_slot=60), dict(k_stride_head=0), dict(v_stride_page=1024),
+    dict(v_stride_page=-4096), dict(k_stride_page=2 ** 61),
+]
+
+
+@pytest.mark.parametrize("kw", BAD_CACHES, ids=lambda k: "-".join(map(str, k.items())))
+def test_caches_that_are_refused(lib, kw):
+    c = fake(**kw)
+    assert call_append(lib, c) == ops.ATTN_ERR_INVALID_ARG
+    assert lib.attn_kv_fork(c, 0x6000000, 0x6100000, 1, 0x5100000, None) == ops.ATTN_ERR_INVALID_ARG
+    assert lib.attn_kv_compact(c, 0x6000000, 0x6100000, 1, 0x6200000, 0x5100000, None) == ops.ATTN_ERR_INVALID_ARG
+
+
+def test_pointers_and_counts_that_are_refused(lib):
+    null, mis, inv = ops.ATTN_ERR_NULL_PTR, ops.ATTN_ERR_MISALIGNED, ops.ATTN_ERR_INVALID_ARG
+    for kw in (dict(k=None), dict(v=None), dict(page_table=None), dict(seq_lens=None), dict(ref_counts=None)):
+        assert call_append(lib, fake(**kw)) == null
+    for kw in (dict(k=0x1000008), dict(v=0x2000002), dict(page_table=0x3000002), dict(ref_counts=0x3200001)):
+        assert call_append(lib, fake(**kw)) == mis
+    assert call_append(lib, fake(), k=None) == null and call_append(lib, fake(), cu=None) == null
+    assert call_append(lib, fake(), status=None) == null
+    assert call_append(lib, fake(), k=0x4000004) == mis and call_append(lib, fake(), cu=0x5000002) == mis
+    assert call_append(lib, fake(), n=-1) == inv and call_append(lib, fake(), stride=4) == inv
+    assert call_append(lib, fake(), stride=-128) == inv
+    assert call_append(lib, fake(v=0x1000000)) == inv  # K and V in one place
+    assert lib.attn_kv_fork(fake(), 0x6000000, 0x6100000, 5, 0x5100000, None) == inv  # more children than rows
+    assert lib.attn_kv_fork(fake(), None, 0x6100000, 1, 0x5100000, None) == null
+    assert lib.attn_kv_fork(fake(), 0x6000000, 0x6100000, 1, None, None) == null
+    assert lib.attn_kv_compact(fake(), 0x6000000, None, 1, 0x6200000, 0x5100000, None) == null
+    assert lib.attn_kv_compact(fake(), 0x6000000, 0x6100000, -1, 0x6200000, 0x5100000, None) == inv
+    assert lib.attn_kv_free(fake(), None, 1, None) == null
+    assert lib.attn_kv_free(fake(), 0x6000000, -1, None) == inv
+    assert lib.attn_kv_free(fake(k=None, v=None), 0x6000000, 0, None) == ops.ATTN_OK  # nothing listed
+    assert lib.attn_kv_free(fake(rows=0), None, 0, None) == ops.ATTN_OK
+    assert lib.attn_kv_append(None, 0x4000000, 0x4100000, 128, 64, 128, 64, 4, 0x5000000, 0x5100000, None) == null
+    assert lib.attn_kv_strerror(999) == b"unknown status"
+
+
+def test_the_binding_refuses_what_is_not_a_cuda_tensor():
+    cache = empty_cache(4, 2, 16, 64, 2, 2, device="cpu")
+    x = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        ops.kv_append(x, x, *cache, i32([0, 1, 1], "cpu"))
+    with pytest.raises(ValueError):
+        ops.kv_free(*cache[2:], i32([0], "cpu"), 16)
+
+
+def test_layouts_of_the_model():
+    for layout in ("heads", "slots", "pairs"):
+        k, v = pool(3, 2, 16, 64, layout, device="cpu")
+        assert k.shape == v.shape == (3, 2, 16, 64) and k.stride(3) == 1
+    assert ctypes.sizeof(_lib.KvCache) == 112
