@@ -29,7 +29,7 @@ class KvCache(ctypes.Structure):
 _cache, _i64 = ctypes.POINTER(KvCache), ctypes.c_int64
 
 # name -> (restype, argtypes), mirroring include/attn_fwd.h, include/attn_fwd_trace.h, include/attn_bwd.h,
-# include/attn_bwd_trace.h, include/attn_kv.h and include/attn_fwd_probe.h
+# include/attn_bwd_trace.h, include/attn_kv.h, include/attn_paged.h and include/attn_fwd_probe.h
 SIGNATURES = {
     "attn_fwd": {
         "attn_fwd": (_c_int, [_vp, _vp, _vp, _vp, _vp] + [_c_int] * 7 + [_c_float, _vp]),
@@ -62,6 +62,13 @@ SIGNATURES = {
         "attn_kv_compact": (_c_int, [_cache, _vp, _vp, _c_int, _vp, _vp, _vp]),
         "attn_kv_free": (_c_int, [_cache, _vp, _c_int, _vp]),
         "attn_kv_strerror": (ctypes.c_char_p, [_c_int]),
+    },
+    "attn_paged": {
+        "attn_fwd_tree": (_c_int, [_cache, _vp, _i64, _i64, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_int, _c_int, _c_int,
+                                   _c_float, _vp, ctypes.c_size_t, _vp]),
+        "attn_fwd_tree_workspace_size": (ctypes.c_size_t, [_c_int]),
+        "attn_paged_strerror": (ctypes.c_char_p, [_c_int]),
+        "attn_paged_debug_status": (_c_int, [_vp, ctypes.POINTER(_c_int)]),
     },
     "attn_probe": {
         "attn_probe_mma_ss": (_c_int, [_vp, _c_int, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp]),

@@ -5,6 +5,7 @@
     libattn_bwd.so        its backward (C ABI: include/attn_bwd.h)
     libattn_bwd_trace.so  the same with the backward kernels' timeline recorded (-DATTN_TRACE; include/attn_bwd_trace.h)
     libattn_kv.so         paged key/value cache: append, fork, compact, free (include/attn_kv.h)
+    libattn_paged.so      attention over such a cache (include/attn_paged.h)
     libattn_probe.so      primitive checks of their building blocks (include/attn_fwd_probe.h)
 
 The translation units compile in parallel; a library is rebuilt only when a
@@ -37,6 +38,7 @@ LIBS = {  # name -> (source, extra nvcc flags)
     "attn_bwd": (os.path.join(CSRC, "attn_bwd.cu"), []),
     "attn_bwd_trace": (os.path.join(CSRC, "attn_bwd.cu"), ["-DATTN_TRACE"]),
     "attn_kv": (os.path.join(CSRC, "kv_pages.cu"), []),
+    "attn_paged": (os.path.join(CSRC, "attn_paged.cu"), []),
     "attn_probe": (os.path.join(CSRC, "probe.cu"), []),
 }
 

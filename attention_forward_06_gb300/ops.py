@@ -497,6 +497,79 @@ def kv_free(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.
     _check_kv(load("attn_kv").attn_kv_free(cache, rows.data_ptr(), n, _stream_handle(stream)))
 
 
+def pack_tree_mask(visible: torch.Tensor) -> torch.Tensor:
+    """Bit-pack a bool ``[tokens, n]`` (which of its sequence's newest tokens each token sees) into the int32 words
+    ``[tokens, ceil(n/32)]`` of ``attn_fwd_tree`` (bit ``i % 32`` of word ``i // 32``), on its device."""
+    if visible.dim() != 2 or visible.dtype != torch.bool:
+        raise ValueError("visible must be a 2-d bool tensor [tokens, newest tokens]")
+    T, n = visible.shape
+    W = (n + 31) // 32
+    padded = torch.zeros((T, W * 32), dtype=torch.int64, device=visible.device)
+    padded[:, :n] = visible
+    words = (padded.view(T, W, 32) << torch.arange(32, device=visible.device)).sum(-1)
+    return torch.where(words >= 1 << 31, words - (1 << 32), words).to(torch.int32)
+
+
+def tree_workspace_size(D: int) -> int:
+    return int(load("attn_paged").attn_fwd_tree_workspace_size(D))
+
+
+def attn_fwd_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor,
+                  seq_lens: torch.Tensor, cu_tokens: torch.Tensor, tree_mask: torch.Tensor | None = None,
+                  window: int = 0, sinks: int = 0, scale: float | None = None, o: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of each sequence's newest tokens over a paged cache: ``(o [tokens, Hq, D], lse [tokens, Hq])``.
+
+    ``q [tokens, Hq, D]`` (bf16, last stride 1) holds row b's tokens at ``cu_tokens[b] : cu_tokens[b+1]``; their K and V
+    are already the last ones of the row's ``seq_lens[b]`` in the cache (``kv_append``).  A token sees its row's
+    context and, of the newest tokens, those up to itself, or those its ``tree_mask`` words mark (``pack_tree_mask``).
+    ``window > 0`` keeps keys nearer than that and the first ``sinks``.  Tokens of no row keep what ``o`` and ``lse``
+    hold.  ``workspace`` (contiguous, ``tree_workspace_size`` bytes) is allocated here when not given.
+    """
+    dev = _on_device(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
+                     cu_tokens=cu_tokens, tree_mask=tree_mask, o=o, lse=lse, workspace=workspace)
+    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens)
+    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != cache.D:
+        raise ValueError(f"q must be a bf16 tensor [tokens, Hq, {cache.D}] whose last stride is 1")
+    T, Hq, D = q.shape
+    _int32("cu_tokens", cu_tokens, cache.rows + 1)
+    words = 0
+    if tree_mask is not None:
+        if tree_mask.element_size() != 4 or tree_mask.dim() != 2 or tree_mask.shape[0] != T or \
+                not tree_mask.is_contiguous():
+            raise ValueError(f"tree_mask must be a contiguous 32-bit tensor [{T}, words]")
+        words = tree_mask.shape[1]
+    if o is None:
+        o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
+    elif tuple(o.shape) != (T, Hq, D) or o.dtype != torch.bfloat16 or not o.is_contiguous():
+        raise ValueError("o must be a contiguous bf16 tensor shaped like q")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    elif tuple(lse.shape) != (T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous fp32 tensor [tokens, Hq]")
+    lib = load("attn_paged")
+    if workspace is None:
+        workspace = torch.empty(lib.attn_fwd_tree_workspace_size(D), dtype=torch.uint8, device=dev)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if scale is None:
+        scale = 1.0 / math.sqrt(D)
+    st = lib.attn_fwd_tree(cache, q.data_ptr(), q.stride(0), q.stride(1), o.data_ptr(), lse.data_ptr(), T, Hq,
+                           cu_tokens.data_ptr(), tree_mask.data_ptr() if tree_mask is not None else None, words,
+                           min(int(window), _INT_MAX), min(int(sinks), _INT_MAX), float(scale), workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if st != ATTN_OK:
+        raise AttnError(st, lib.attn_paged_strerror(st).decode())
+    return o, lse
+
+
+def paged_debug_status(stream=None) -> tuple[int, int]:
+    """Synchronise ``stream`` and read/clear the paged attention's status word: ``(status, site)``."""
+    site = ctypes.c_int(0)
+    st = load("attn_paged").attn_paged_debug_status(_stream_handle(stream), ctypes.byref(site))
+    return st, site.value
+
+
 def bwd_debug_status(stream=None) -> tuple[int, int]:
     """Synchronise ``stream`` and read/clear the backward kernels' timeout word: ``(status, site)``."""
     site = ctypes.c_int(0)

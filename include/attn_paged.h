@@ -1,0 +1,87 @@
+/*
+ * attn_paged.h -- C ABI of attention over a paged key/value cache for GB300 (sm_103a):
+ * each sequence's newest tokens (one, a chain, or a tree of drafted tokens) against
+ * the pages of its row of an attn_kv_cache (attn_kv.h).
+ *
+ * Operation.  Row b of the cache has L = seq_lens[b] tokens, of which the newest
+ * n = cu_tokens[b + 1] - cu_tokens[b] are the queries, token u at place
+ * L - n + u of the cache: their K and V are appended before the call.  For query token
+ * t = cu_tokens[b] + u and query head h, with ctx = L - n:
+ *     O[t,h,:] = sum_j P_j V[j],   P_j = exp(scale <Q[t,h,:], K[j]> - LSE[t,h]),
+ *     LSE[t,h] = ln sum_j exp(scale <Q[t,h,:], K[j]>)
+ * over the visible keys j < L of kv head h / (Hq / Hkv).  Visible are
+ *     every key j < ctx (the context), and of the newest tokens
+ *     without tree_mask: those up to the token itself (a chain: j <= ctx + u);
+ *     with tree_mask: token ctx + i iff bit i % 32 of tree_mask[t][i / 32] is set
+ *     (a tree: a token's ancestors and itself; i < n, i < 32 mask_words).
+ * With window > 0 a key also has to be near or a sink.  Without tree_mask that is
+ * attn_fwd_window's rule, p - j < window or j < sinks with p = ctx + u.  With tree_mask it
+ * restricts the context alone, with p = ctx + (visible newest tokens) - 1, the
+ * token's place in the text its ancestors form.
+ * A token without visible keys gets O = 0 and LSE = -inf.  Tokens of q before
+ * cu_tokens[0] and from cu_tokens[rows] on belong to no row: o and lse keep what they hold there.
+ *
+ * Layout.  q: bf16, element (token, head, d) at token * q_stride_token + head *
+ * q_stride_head + d (multiples of 8).  o: bf16 [n_tokens][Hq][D], lse: fp32
+ * [n_tokens][Hq], contiguous.  cu_tokens int32 [rows + 1], tree_mask uint32
+ * [n_tokens][mask_words] or NULL.  D is 64 or 128; Hq a multiple of Hkv, at most 128 query
+ * heads per kv head; scale finite and positive; q, o, lse and the workspace 16-byte
+ * aligned.  o, lse and the workspace must not overlap each other or an input.
+ *
+ * What a page holds behind the row's last token, and pages that no row lists, may be
+ * anything (NaN too): it is not used.  The keys and values of a token that is masked
+ * for another do not reach that one either.  V entries beyond 65504 in magnitude are
+ * clamped for the product (attn_fwd.h, "Precision").
+ *
+ * Lengths and tables lie on the device and are checked there.  A row whose cu_tokens
+ * fall or leave [0, n_tokens] is passed over; one with L < n or L over max_pages *
+ * page_size has its tokens written as without keys; a page number outside [0, n_pages)
+ * reads as zeros.  Each sets the status that attn_paged_debug_status reports.
+ *
+ * Work is cut evenly over the SMs by key tiles whatever the lengths are; a sequence cut
+ * in several ranges is merged by LSE in a second kernel, in a fixed order, so
+ * results are the same from run to run.  Two kernels are enqueued on `stream`;
+ * nothing is allocated and nothing waits for the device.  Calls that may run at the
+ * same time need workspaces of their own.
+ */
+#ifndef ATTN_PAGED_H
+#define ATTN_PAGED_H
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "attn_kv.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Enqueue the attention of n_tokens newest tokens.  Argument checks run on the host
+   before any device work; with rows == 0 or n_tokens == 0 there is nothing to do.
+   window 0: none (sinks is then ignored). */
+int attn_fwd_tree(const attn_kv_cache* cache, const void* q, int64_t q_stride_token, int64_t q_stride_head, void* o,
+                  float* lse, int n_tokens, int Hq, const int32_t* cu_tokens, const uint32_t* tree_mask,
+                  int mask_words, int window, int sinks, float scale, void* workspace, size_t workspace_bytes,
+                  cudaStream_t stream);
+
+/* Workspace bytes attn_fwd_tree needs for heads of D: two partial results per SM,
+   whatever the batch and its lengths; 0 for another D.  Host only, no CUDA call.  Its
+   contents need no preparation. */
+size_t attn_fwd_tree_workspace_size(int D);
+
+/* Text for a status code (ATTN_ERR_CUDA names this library's last CUDA error on the
+   calling thread). */
+const char* attn_paged_strerror(int status);
+
+/* Synchronise `stream`, then read and clear the library's device status word for the
+   current device: ATTN_OK; ATTN_ERR_DEVICE_TIMEOUT when a bounded wait ran out;
+   ATTN_ERR_INVALID_ARG when a call met lengths or page numbers that do not fit (above); or
+   ATTN_ERR_CUDA.  `site` (may be NULL) receives the recorded code. */
+int attn_paged_debug_status(cudaStream_t stream, int* site);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* ATTN_PAGED_H */

@@ -1,0 +1,435 @@
+"""Attention over a paged cache (attn_fwd_tree) against the definition in 64 bits: single tokens, chains and trees of
+drafted tokens; ragged batches, sequences without context and without tokens; pages of every size that end inside a
+tile, in every layout; windows and sinks; masks that leave a row empty; what lies behind a sequence's end (NaN); bad
+lengths and page numbers.
+
+Tolerances are the dense entry points' (parity_util): |dO| <= 1e-2 below 4 and |dLSE| <= 1e-3.  A partial result is
+fp32 and its weight 2^x by an instruction of relative error below 2^-21, so cutting a sequence into ranges adds nothing
+that shows beside the rounding of O to bf16.
+"""
+import os
+import re
+
+import numpy as np
+import pytest
+import torch
+
+from attention_forward_06_gb300 import _lib, ops
+from attention_forward_06_gb300 import build as B
+from paged_model import i32, pool
+from parity_util import compare
+from plain_attention import forward
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+gpu = pytest.mark.gpu
+
+
+def tree(n, rng, reach=6):
+    """bool [n, n]: a random tree's ancestors and self."""
+    vis = np.zeros((n, n), bool)
+    for t in range(n):
+        parent = rng.integers(max(-1, t - reach), t) if t else -1
+        if parent >= 0:
+            vis[t] = vis[parent]
+        vis[t, t] = True
+    return vis
+
+
+class Batch:
+    """A cache with ragged rows, and the queries of their newest tokens."""
+
+    def __init__(self, lens, n, Hq, Hkv, D, P, layout="heads", trees=None, seed=0, spare=3, qk_std=1.0, pad=(0, 0)):
+        rng = np.random.default_rng(seed)
+        self.lens, self.n, self.G, self.D, self.P, self.trees = list(lens), list(n), Hq // Hkv, D, P, trees
+        used = [-(-x // P) for x in lens]
+        n_pages = sum(used) + spare
+        self.k, self.v = pool(n_pages, Hkv, P, D, layout, seed + 1)
+        order = rng.permutation(n_pages)
+        table = np.full((len(lens), max(used + [1]) + 1), -1)
+        at = 0
+        for b, u in enumerate(used):
+            table[b, :u] = order[at:at + u]
+            at += u
+        self.table_np = table
+        self.table, self.seq_lens = i32(table), i32(lens)
+        cu = np.concatenate([[0], np.cumsum(n)]) + pad[0]
+        self.cu_np, self.cu = cu, i32(cu)
+        T = int(cu[-1]) + pad[1]
+        g = torch.Generator().manual_seed(seed + 2)
+        self.q = (torch.randn((T, Hq, D), generator=g) * qk_std).to(torch.bfloat16).cuda()
+        self.mask = None
+        if trees is not None:
+            vis = np.zeros((T, max(max(n), 1)), bool)
+            for c, m, t in zip(cu, n, trees):
+                vis[c:c + m, :m] = t
+            self.mask = ops.pack_tree_mask(torch.as_tensor(vis)).cuda()
+
+    def rows(self, x, b):
+        """Row b's keys (or values) [1, Hkv, len, D]."""
+        pages = torch.as_tensor(self.table_np[b, :-(-self.lens[b] // self.P)], device=x.device)
+        return x[pages].transpose(0, 1).reshape(x.shape[1], -1, self.D)[None, :, :self.lens[b]].cpu()
+
+    def visible(self, b, window, sinks):
+        L, m = self.lens[b], self.n[b]
+        ctx, j = L - m, np.arange(L)
+        vis = np.ones((m, L), bool)
+        own = self.trees[b] if self.trees is not None else np.tril(np.ones((m, m), bool))
+        vis[:, ctx:] = own
+        if window:
+            place = ctx + (own.sum(1) - 1 if self.trees is not None else np.arange(m))
+            near = (place[:, None] - j < window) | (j < sinks)
+            vis &= near | (j >= ctx) if self.trees is not None else near
+        return vis
+
+    def run(self, window=0, sinks=0, scale=None, **kw):
+        o, lse = ops.attn_fwd_tree(self.q, self.k, self.v, self.table, self.seq_lens, self.cu, tree_mask=self.mask,
+                                   window=window, sinks=sinks, scale=scale, **kw)
+        st, site = ops.paged_debug_status()
+        assert st == ops.ATTN_OK, f"status {st} at site {site}"
+        return o, lse
+
+    def check(self, o, lse, window=0, sinks=0, scale=None, only=None):
+        scale = scale or float(np.float32(self.D ** -0.5))
+        for b in range(len(self.lens)) if only is None else only:
+            c0, c1 = self.cu_np[b], self.cu_np[b + 1]
+            if c0 == c1:
+                continue
+            q = self.q[c0:c1].transpose(0, 1)[None].cpu()
+            ref = forward(q, self.rows(self.k, b), self.rows(self.v, b), self.visible(b, window, sinks), scale)
+            compare(o[c0:c1].transpose(0, 1)[None], lse[c0:c1].T[None], *ref)
+
+    def whole(self, window=0, sinks=0, scale=None):
+        self.check(*self.run(window, sinks, scale), window, sinks, scale)
+
+
+CASES = [
+    # lens, n, Hq, Hkv, D, P, layout, tree, window, sinks
+    ([1], [1], 1, 1, 128, 16, "heads", False, 0, 0),                      # one key, itself
+    ([17], [1], 8, 2, 64, 16, "heads", False, 0, 0),
+    ([128, 129, 127], [1, 1, 1], 4, 1, 128, 64, "slots", False, 0, 0),    # a tile's edges
+    ([5000, 1, 333, 2, 64], [1, 1, 1, 1, 1], 32, 8, 128, 16, "heads", False, 0, 0),
+    ([3000, 700], [1, 1], 6, 1, 64, 256, "pairs", False, 0, 0),           # six heads share a kv head
+    ([900, 40, 0, 77], [3, 40, 0, 0], 8, 2, 128, 32, "heads", False, 0, 0),  # no context; no tokens
+    ([700], [300], 4, 2, 128, 128, "slots", False, 0, 0),                 # a chunk over several row tiles
+    ([400, 1200], [64, 23], 32, 8, 128, 32, "heads", True, 0, 0),         # drafted trees
+    ([200, 45], [100, 45], 16, 1, 64, 16, "pairs", True, 0, 0),           # ... and without context
+    ([350], [33], 127, 1, 64, 64, "heads", True, 0, 0),                   # one token per row tile
+    ([260], [2], 128, 1, 128, 64, "heads", False, 0, 0),
+    ([4000, 100], [1, 1], 8, 8, 64, 128, "heads", False, 500, 4),         # a window and sinks
+    ([4000, 2500], [7, 1], 8, 2, 128, 16, "heads", False, 129, 130),      # sinks past a tile, chain
+    ([1500], [200], 4, 4, 128, 64, "slots", False, 64, 0),                # a window shorter than the chain
+    ([3000, 90], [40, 40], 8, 2, 64, 32, "heads", True, 300, 3),          # a tree's places in its window
+    ([800], [5], 4, 1, 128, 16, "heads", False, 10 ** 9, 7),
+    ([800], [5], 4, 1, 128, 16, "heads", False, 1, 0),                    # each token sees itself alone
+]
+
+
+@gpu
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "x".join(map(str, (c[0][:3], c[1][:3], *c[2:]))))
+def test_matches_the_definition(case):
+    lens, n, Hq, Hkv, D, P, layout, is_tree, window, sinks = case
+    rng = np.random.default_rng(len(lens) + D)
+    trees = [tree(m, rng) for m in n] if is_tree else None
+    Batch(lens, n, Hq, Hkv, D, P, layout, trees, seed=sum(n)).whole(window, sinks)
+
+
+@gpu
+@pytest.mark.parametrize("seed", range(12))
+def test_random_batches(seed):
+    rng = np.random.default_rng(100 + seed)
+    rows, D, P = int(rng.integers(1, 40)), int(rng.choice([64, 128])), int(rng.choice([16, 32, 64, 128, 256]))
+    Hkv, G = [(1, 8), (2, 4), (4, 6), (8, 1), (3, 5)][seed % 5]
+    n = rng.integers(0, 2 if seed % 3 == 0 else 60, rows)
+    lens = n + rng.integers(0, 1500, rows) * rng.integers(0, 2, rows)
+    trees = [tree(m, rng) for m in n] if seed % 2 else None
+    window = int(rng.integers(1, 900)) if seed % 4 >= 2 else 0
+    Batch(lens, n, Hkv * G, Hkv, D, P, ["heads", "slots", "pairs"][seed % 3], trees, seed, qk_std=1 + seed % 3,
+          pad=(seed % 2, seed % 3)).whole(window, int(rng.integers(0, 9)))
+
+
+@gpu
+def test_a_growing_maximum_moves_the_reference_value():
+    # keys that grow along the sequence, by more than fp16 holds above the first tile's
+    b = Batch([3000, 2000], [2, 1], 4, 1, 128, 64, seed=3)
+    for row in range(2):
+        for at, page in enumerate(b.table_np[row, :-(-b.lens[row] // 64)]):
+            b.k[page] *= 0.2 + 0.15 * at
+    b.whole()
+
+
+@gpu
+def test_masks_that_leave_a_row_empty():
+    # token 0 sees nothing at all (no context), token 1 the context's sinks alone, bits past the tokens are ignored
+    lens, n = [5, 700], [5, 3]
+    trees = [np.tril(np.ones((5, 5), bool), -1), np.zeros((3, 3), bool)]
+    b = Batch(lens, n, 8, 2, 64, 16, trees=trees, seed=4)
+    b.mask[5:] |= ~7  # bits 3 .. 31 of the second row's tokens
+    o, lse = b.run(window=4, sinks=2)
+    b.check(o, lse, 4, 2)
+    assert torch.all(o[0] == 0) and torch.all(torch.isneginf(lse[0]))
+
+
+@gpu
+def test_what_a_page_holds_behind_the_sequence_is_not_used():
+    b = Batch([130, 40, 300], [4, 1, 30], 8, 2, 128, 64, seed=5)
+    want = b.run()
+    for x in (b.k, b.v):
+        free = torch.ones(x.shape[0], dtype=torch.bool)
+        for row, length in enumerate(b.lens):
+            pages = b.table_np[row, :-(-length // 64)]
+            free[pages] = False
+            if length % 64:
+                x[pages[-1], :, length % 64:] = float("nan")
+        x[free.cuda()] = float("inf")
+    got = b.run()
+    assert all(torch.equal(a, c) for a, c in zip(want, got))
+
+
+@gpu
+def test_nan_reaches_the_tokens_that_see_it_alone():
+    # the second of three sibling drafts has NaN in its V, a context key of the other row too
+    trees = [np.eye(3, dtype=bool), np.ones((1, 1), bool)]
+    b = Batch([600, 500], [3, 1], 4, 2, 128, 16, trees=trees, seed=6)
+    want, want_lse = b.run()
+    at = 600 - 2
+    b.v[b.table_np[0, at // 16], 1, at % 16, 7] = float("nan")
+    b.v[b.table_np[1, 3], 0, 2] = float("nan")
+    o, lse = b.run()
+    hit = torch.zeros_like(want, dtype=torch.bool)
+    hit[1, 2:] = True   # the draft's heads of kv head 1
+    hit[3, :2] = True   # the other row's heads of kv head 0
+    assert torch.equal(torch.isnan(o), hit) and torch.equal(o[~hit], want[~hit]) and torch.equal(lse, want_lse)
+
+
+@gpu
+def test_tokens_of_no_row_keep_what_they_hold():
+    b = Batch([200, 300], [1, 4], 4, 1, 64, 32, seed=7, pad=(3, 6))
+    o = torch.full((14, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((14, 4), 9.0, device="cuda")
+    b.run(o=o, lse=lse)
+    b.check(o, lse)
+    for rows in (slice(0, 3), slice(8, 14)):
+        assert torch.all(o[rows] == 7) and torch.all(lse[rows] == 9)
+
+
+@gpu
+def test_queries_as_a_slice_of_a_fused_projection_and_a_given_scale():
+    b = Batch([400, 90], [2, 9], 8, 2, 64, 16, seed=8)
+    fused = torch.zeros((11, 12 * 64), dtype=torch.bfloat16, device="cuda")
+    fused[:, 128:640] = b.q.reshape(11, 512)
+    b.q = fused[:, 128:640].view(11, 8, 64)
+    b.whole(scale=0.3)
+
+
+@gpu
+def test_lengths_and_pages_that_do_not_fit_are_reported():
+    good = Batch([100, 300, 50], [2, 2, 2], 4, 1, 64, 16, seed=9)
+    call = lambda **kw: ops.attn_fwd_tree(good.q, good.k, good.v, kw.get("table", good.table),  # noqa: E731
+                                          kw.get("lens", good.seq_lens), kw.get("cu", good.cu),
+                                          o=torch.full((6, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda"))
+    # more tokens than keys, and more keys than the table holds: written as rows without keys
+    for bad in (1, 16 * good.table.shape[1] + 1, -5, 2 ** 31 - 1):
+        o, lse = call(lens=i32([100, bad, 50]))
+        assert ops.paged_debug_status()[0] == ops.ATTN_ERR_INVALID_ARG
+        assert torch.all(o[2:4] == 0) and torch.all(torch.isneginf(lse[2:4]))
+        good.check(o, lse, only=[0, 2])
+    # tokens out of range: the row is passed over
+    for cu in ([0, 2, 1, 6], [0, 2, 9, 6], [-1, 2, 4, 6], [0, 2, 4, 2 ** 31 - 1]):
+        call(cu=i32(cu))
+        assert ops.paged_debug_status()[0] == ops.ATTN_ERR_INVALID_ARG
+    # page numbers past the pool read as zeros
+    for page in (-1, good.k.shape[0], 2 ** 31 - 1, -2 ** 31):
+        table = good.table.clone()
+        table[1, 1] = page
+        o, lse = call(table=table)
+        assert ops.paged_debug_status()[0] == ops.ATTN_ERR_INVALID_ARG
+        assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+        good.check(o, lse, only=[0, 2])
+    o, lse = call()
+    assert ops.paged_debug_status()[0] == ops.ATTN_OK  # reported once
+    good.check(o, lse)
+
+
+@gpu
+def test_the_same_twice_in_a_graph_and_on_another_stream():
+    trees = [tree(m, np.random.default_rng(m)) for m in (30, 7, 0)]
+    b = Batch([900, 2300, 10], [30, 7, 0], 16, 4, 128, 32, trees=trees, seed=10)
+    want = b.run()
+    ws = torch.empty(ops.tree_workspace_size(128), dtype=torch.uint8, device="cuda")
+    assert all(torch.equal(x, y) for x, y in zip(want, b.run(workspace=ws.fill_(255))))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = ops.attn_fwd_tree(b.q, b.k, b.v, b.table, b.seq_lens, b.cu, tree_mask=b.mask)
+    side.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want, got))
+    # a captured call follows the lengths and tables that it finds at each replay
+    graph, lens0 = torch.cuda.CUDAGraph(), b.seq_lens.clone()
+    with torch.cuda.graph(graph):
+        out = ops.attn_fwd_tree(b.q, b.k, b.v, b.table, b.seq_lens, b.cu, tree_mask=b.mask, workspace=ws)
+    for lens in ([31, 2000, 10], [900, 2300, 10]):
+        b.seq_lens.copy_(i32(lens))
+        b.lens = lens
+        graph.replay()
+        torch.cuda.synchronize()
+        b.check(*out)
+    assert torch.equal(b.seq_lens, lens0) and all(torch.equal(x, y) for x, y in zip(want, out))
+
+
+@gpu
+def test_many_rows():
+    rng = np.random.default_rng(11)
+    n = rng.integers(0, 3, 700)
+    Batch(n + rng.integers(0, 40, 700), n, 4, 2, 64, 16, seed=11).whole()
+
+
+@gpu
+def test_offsets_past_32_bits():
+    # a pool of more than 2^31 elements per tensor, and a sequence in its last pages
+    n_pages, Hkv, P, D = 16500, 8, 128, 128
+    if torch.cuda.mem_get_info()[0] < (16 << 30):
+        pytest.skip("needs 16 GB of free device memory")
+    b = Batch([700], [2], 16, Hkv, D, P, seed=12)
+    want = b.run()
+    for name in "kv":
+        x = getattr(b, name)
+        big = torch.zeros((n_pages, Hkv, P, D), dtype=torch.bfloat16, device="cuda")
+        big[n_pages - x.shape[0]:] = x
+        setattr(b, name, big)
+        del x, big
+    b.table = torch.where(b.table >= 0, b.table + (n_pages - 9), b.table)
+    assert b.k.numel() > 2 ** 31
+    assert all(torch.equal(x, y) for x, y in zip(want, b.run()))
+
+
+@gpu
+def test_a_speculative_step_end_to_end():
+    """Append a prompt, decode; fork the row, append drafted tokens, attend as a tree, keep the accepted ones, attend
+    again: each output against the definition over the tokens that the row then holds."""
+    Hq, Hkv, D, P, L = 8, 2, 128, 32, 150
+    rows, g = 3, torch.Generator().manual_seed(13)
+    draw = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16)  # noqa: E731
+    k, v = pool(40, Hkv, P, D, seed=1)
+    cache = (k, v, torch.full((rows, 12), -1, dtype=torch.int32, device="cuda"), i32([0] * rows), i32([0] * 40))
+    text = [[draw(0, Hkv, D), draw(0, Hkv, D)] for _ in range(rows)]
+    scale = float(np.float32(D ** -0.5))
+
+    def append(n):
+        kn, vn = draw(sum(n), Hkv, D), draw(sum(n), Hkv, D)
+        cu = np.concatenate([[0], np.cumsum(n)])
+        assert ops.kv_append(kn.cuda(), vn.cuda(), *cache, i32(cu)).item() == 0
+        for b in range(rows):
+            text[b] = [torch.cat([t, x[cu[b]:cu[b + 1]]]) for t, x in zip(text[b], (kn, vn))]
+        return cu
+
+    def attend(cu, trees=None):
+        q, mask = draw(int(cu[-1]), Hq, D), None
+        if trees is not None:
+            vis = np.zeros((int(cu[-1]), max(len(t) for t in trees)), bool)
+            for b, t in enumerate(trees):
+                vis[cu[b]:cu[b + 1], :len(t)] = t
+            mask = ops.pack_tree_mask(torch.as_tensor(vis)).cuda()
+        o, lse = ops.attn_fwd_tree(q.cuda(), *cache[:4], i32(cu), tree_mask=mask)
+        assert ops.paged_debug_status()[0] == ops.ATTN_OK
+        for b in range(rows):
+            m, total = int(cu[b + 1] - cu[b]), len(text[b][0])
+            if m == 0:
+                continue
+            vis = np.ones((m, total), bool)
+            vis[:, total - m:] = trees[b] if trees is not None else np.tril(np.ones((m, m), bool))
+            ref = forward(q[cu[b]:cu[b + 1]].transpose(0, 1)[None], *[t.transpose(0, 1)[None] for t in text[b]], vis,
+                          scale)
+            compare(o[cu[b]:cu[b + 1]].transpose(0, 1)[None], lse[cu[b]:cu[b + 1]].T[None], *ref)
+
+    attend(append([L, 0, 0]))
+    assert ops.kv_fork(*cache, i32([0, 0]), i32([1, 2])).item() == 0
+    text[1], text[2] = [list(t) for t in (text[0], text[0])]
+    attend(append([1, 1, 1]))
+    rng = np.random.default_rng(14)
+    n = [9, 33, 0]
+    cu = append(n)
+    attend(cu, [tree(m, rng) for m in n])
+    acc = [[0, 3, 8], [1, 2, 30], []]
+    ends = np.concatenate([[0], np.cumsum([len(a) for a in acc])])
+    assert not ops.kv_compact(*cache, i32(cu), i32(sum(acc, [])), i32(ends)).any()
+    for b in range(rows):
+        keep = list(range(len(text[b][0]) - n[b])) + [len(text[b][0]) - n[b] + a for a in acc[b]]
+        text[b] = [t[keep] for t in text[b]]
+    attend(append([1, 1, 5]))
+    ops.kv_free(*cache[2:], i32([0, 1, 2]), P)
+    assert not cache[4].any() and not cache[3].any()
+
+
+# ---------------------------------------------------------------------------- on the CPU
+@pytest.fixture(scope="module")
+def lib():
+    B.build()
+    return _lib.load("attn_paged")
+
+
+def test_exports_what_the_header_declares(lib):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include/attn_paged.h")).read(), flags=re.S)
+    funcs = set(re.findall(r"^\s*(?:const\s+)?\w+\s*\*?\s*(attn_\w+)\s*\(", text, flags=re.M))
+    assert funcs == set(_lib.SIGNATURES["attn_paged"]) and len(funcs) == 4
+    assert all(hasattr(lib, f) for f in funcs)
+
+
+def test_workspace_size(lib):
+    for D in (64, 128):
+        # 192 CTAs: two partials of 128 rows (D values and an LSE each), and 16 bytes
+        assert ops.tree_workspace_size(D) == 192 * (2 * 128 * (D + 1) * 4 + 16)
+    assert lib.attn_fwd_tree_workspace_size(96) == 0
+
+
+def fake(**kw):
+    """A cache at addresses that are never read: the host's checks come first."""
+    a = dict(k=0x1000000, v=0x2000000, k_stride_page=2 * 16 * 64, k_stride_head=16 * 64, k_stride_slot=64,
+             v_stride_page=2 * 16 * 64, v_stride_head=16 * 64, v_stride_slot=64, page_table=0x3000000,
+             seq_lens=0x3100000, ref_counts=None, n_pages=10, Hkv=2, page_size=16, D=64, rows=4, max_pages=5)
+    return _lib.KvCache(**dict(a, **kw))
+
+
+def call(lib, cache=None, **kw):
+    a = dict(q=0x4000000, q_token=512, q_head=64, o=0x5000000, lse=0x6000000, T=6, Hq=8, cu=0x7000000, mask=0x7100000,
+             words=1, window=0, sinks=0, scale=0.1, ws=0x8000000, n=1 << 30)
+    a.update(kw)
+    return lib.attn_fwd_tree(cache if cache is not None else fake(), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw", [dict(Hq=7), dict(Hq=0), dict(Hq=258), dict(T=-1), dict(window=-1), dict(sinks=-1),
+                                dict(scale=0.0), dict(scale=float("inf")), dict(words=0), dict(mask=None),
+                                dict(q_token=4), dict(q_head=-64), dict(n=1000), dict(o=0x4000000), dict(lse=0x5000000),
+                                dict(ws=0x1000000), dict(ws=0x4000000), dict(o=0x3000000 - 64), dict(o=0x7100000)],
+                         ids=lambda k: "-".join(map(str, k.items())))
+def test_arguments_that_are_refused(lib, kw):
+    assert call(lib, **kw) == ops.ATTN_ERR_INVALID_ARG
+
+
+def test_caches_and_pointers_that_are_refused(lib):
+    for kw in (dict(D=96), dict(page_size=24), dict(Hkv=0), dict(rows=40000), dict(k_stride_slot=8)):
+        assert call(lib, fake(**kw)) == ops.ATTN_ERR_INVALID_ARG
+    for kw in (dict(q=None), dict(o=None), dict(lse=None), dict(cu=None), dict(ws=None)):
+        assert call(lib, **kw) == ops.ATTN_ERR_NULL_PTR
+    for kw in (dict(k=None), dict(page_table=None), dict(seq_lens=None)):
+        assert call(lib, fake(**kw)) == ops.ATTN_ERR_NULL_PTR
+    for kw in (dict(q=0x4000008), dict(o=0x5000002), dict(lse=0x6000004), dict(cu=0x7000001), dict(mask=0x7100002),
+               dict(ws=0x8000008)):
+        assert call(lib, **kw) == ops.ATTN_ERR_MISALIGNED
+    # nothing to do: no CUDA call
+    assert call(lib, T=0) == ops.ATTN_OK and call(lib, fake(rows=0)) == ops.ATTN_OK
+
+
+def test_pack_tree_mask_by_hand():
+    vis = np.random.default_rng(1).random((5, 70)) < 0.5
+    words = ops.pack_tree_mask(torch.as_tensor(vis)).numpy().view(np.uint32)
+    assert words.shape == (5, 3)
+    for t in range(5):
+        for i in range(96):
+            assert (words[t, i // 32] >> (i % 32)) & 1 == (vis[t, i] if i < 70 else 0)
+
+
+def test_the_binding_refuses_what_is_not_a_cuda_tensor():
+    k, v = pool(3, 2, 16, 64, device="cpu")
+    q = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        ops.attn_fwd_tree(q, k, v, i32([[0]], "cpu"), i32([3], "cpu"), i32([0, 1], "cpu"))
