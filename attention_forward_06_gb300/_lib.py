@@ -26,7 +26,7 @@ class KvCache(ctypes.Structure):
                 + [(n, ctypes.c_int32) for n in ("n_pages", "Hkv", "page_size", "D", "rows", "max_pages")])
 
 
-_cache, _i64 = ctypes.POINTER(KvCache), ctypes.c_int64
+_cache, _i64 = _vp, ctypes.c_int64  # an attn_kv_cache: byref(KvCache(..)), or its bytes
 
 # name -> (restype, argtypes), mirroring include/attn_fwd.h, include/attn_fwd_trace.h, include/attn_bwd.h,
 # include/attn_bwd_trace.h, include/attn_kv.h, include/attn_paged.h and include/attn_fwd_probe.h

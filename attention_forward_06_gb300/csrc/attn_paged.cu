@@ -4,31 +4,50 @@
 // heads of a group) the cache's bytes take longer than the tensor cores.
 //
 // attn_tree_kernel: one persistent CTA per SM.  The work is a list of key tiles (128
-// keys of one kv head) ordered by sequence, 128-row tile, kv head and tile;
-// every CTA takes an equal, contiguous part of it, found from the lengths on the device
-// (one warp sums the sequences' tiles), so the load is even whatever the lengths are and
-// the host needs none of them.  The 128 rows are the tokens of a sequence times the G query
-// heads of a kv head.  An item is the part of one (rows, kv head)'s tiles that a CTA holds;
-// one that holds all of them writes O and LSE, otherwise it leaves a normalised fp32
-// partial and its LSE in the workspace (at most two per CTA: the item it
-// begins with and the item it ends with), which attn_tree_merge_kernel joins.
+// keys of one kv head) ordered by sequence, rows, kv head and tile; every CTA takes an
+// equal, contiguous part of it, found from the lengths on the device (one warp sums the
+// sequences' tiles), so the load is even whatever the lengths are and the host needs none
+// of them.  Rows are the tokens of a sequence times the G query heads of a kv head, in row
+// tiles of 128.  An item is the part of one (row tile, kv head)'s key tiles that a CTA
+// holds; one that holds all of them writes O and LSE, otherwise it leaves a normalised fp32
+// partial and its LSE in the workspace (at most two per CTA: the item it begins with and
+// the item it ends with), which attn_tree_merge_kernel joins.
 //
 // Twelve warps:
-//   warps 0-3    softmax, one thread per row, and the epilogue
-//   warps 4-7    V tiles from bf16 to fp16 in place, rows past the sequence zeroed
-//   warp  8      TMA producer: K and V pages into a ring of tile slots
-//   warp  9      tcgen05 issuer and TMEM owner
-//   warps 10-11  Q rows into one of two buffers
-// TMEM: S of even steps [0,128), of odd steps [128,256), O [256, 256 + D); P (fp16) over
-// the last 64 columns of its S.  The issuer runs S one step ahead:
-//   S(0) | S(g+1) PV(g) | S(g+2) PV(g+1) | ...   across items,
-// so S(g+1) is ready when the softmax has handed over P(g).
+//   warps 0-3   softmax and the epilogue
+//   warps 4-7   V tiles from bf16 to fp16 in place, rows past the sequence zeroed
+//   warp  8     the plan; TMA of K pages into a ring of tile slots
+//   warp  9     tcgen05 issuer and TMEM owner
+//   warp  10    TMA of V pages into a ring of its own (in one stream with K, K would wait for
+//               slots of V and arrive late: 404 us where this takes 240)
+//   warp  11    TMA of the Q rows
+// Pairs (PAIR).  With more tokens than a row tile holds an item is two row tiles that share
+// each K and V tile: warps 0-3 and 4-7 take one each and convert half of V each.  Eight
+// trees of 32 to 64 tokens, 4 heads per kv head, up to 16384 keys, D 128: 130 us, against
+// 152 with the row tiles apart, which read K and V twice.
+// Key groups.  A thread of a softmax warp sees one TMEM lane, one row; with 32 rows or
+// fewer (a token or a few per sequence) three of the four warps would idle while one takes
+// the exponentials of all 128 keys.  So such an item's rows are repeated in the lanes of all four
+// warps, and warp w takes keys 32 w .. 32 w + 31 of every tile and writes P = 0 for the
+// others: each warp's lanes then accumulate O over its keys, against an m of their
+// own, and the epilogue joins the four (two groups of 64 keys up to 64 rows).
+// TMEM: S of even products [0,128), of odd products [128,256), O of the row tiles [256, 256 + D)
+// and the D columns after it, P (fp16 pairs) [384,448) and [448,512), or over its S (a pair at D 128).
 //
 // Softmax as attn_fwd.cu's: exponentials in log2 units against a reference value m that
-// all of a row's sums share.  Here every tile's max is taken (the time is there) and m is
-// moved only when P would pass 2^15: it is set 6 below the tile's max, so P of
-// the largest key starts at 2^6 and fp16 keeps keys down to 2^-20 of it in full precision,
-// 2^-30 at all.  O is then scaled in TMEM after PV(g-1) has finished.
+// all of a row's sums share.  m is set 6 below the max of the row's first keys, so P of the
+// largest key starts at 2^6 and fp16 keeps keys down to 2^-20 of it in full precision, 2^-30 at
+// all.  Later tiles are taken against the same m, without their max; where 32 keys' sum of P
+// passes fp16's largest value m moves to 6 below their max, and P, the sums and O (in TMEM,
+// once the PV before has finished) are scaled.
+//
+// Measured (graph of 20 calls, both kernels): 64 sequences of up to 8192 keys, one token each,
+// 32 / 8 heads, D 128: 240 us, 6.8 TB/s of K and V, the card's copy rate.  32 sequences, a window
+// of 4096 and 4 sinks, 16 heads, D 64: 109 us (4.9 TB/s: items of 33 tiles, whose ends show).
+// One token over 2048 keys: 14.8 us, the latency of the plan, two loads, a tile and the merge.
+// The loops over columns and chunks are rolled: with twelve warps of five kinds the instruction
+// cache is what unrolled code waits for (the trees took 210 us with 64 columns at a time, 163
+// with 32).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -37,6 +56,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "attn_paged.h"
 #include "host_util.h"
@@ -47,44 +67,50 @@ using namespace attn;
 
 namespace {
 
-constexpr int BM = 128;  // rows (tokens x heads of a group) per item
+constexpr int BM = 128;  // rows (tokens x heads of a group) per row tile
 constexpr int BN = 128;  // keys per tile
 constexpr int kThreads = 384;
-constexpr int kLoadWarp = 8;
+constexpr int kKeyWarp = 8;
 constexpr int kMmaWarp = 9;
-constexpr uint32_t kRegsLaunch = 168;   // 65536 / 384
-constexpr uint32_t kRegsSoftmax = 232;  // a whole S row lives in registers
-constexpr uint32_t kRegsConvert = 136;
-constexpr uint32_t kRegsOther = 136;
-static_assert(128 * (kRegsSoftmax + kRegsConvert + kRegsOther) <= kThreads * kRegsLaunch, "register split");
+constexpr int kValueWarp = 10;
+constexpr uint32_t kRegsLaunch = 168;  // 65536 / 384
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kTmemO = 2 * BN;
+constexpr uint32_t kTmemO = 2 * BN;  // columns: S of even and odd products, O of the row tiles, P
+constexpr uint32_t kTmemP = 3 * BN;
 constexpr uint64_t kTimeoutNs = 4000000000ull;
 constexpr uint64_t kDrainTimeoutNs = 500000000ull;
-constexpr float kStart = 6.0f;   // log2 of P of the largest key when m is set
-constexpr float kLimit = 15.0f;  // log2 of P at which m moves (fp16 holds up to 2^16)
-constexpr int kMaxCtas = 192;    // partial slots are sized for this many CTAs
+constexpr float kStart = 6.0f;       // log2 of P of the largest key when m is set
+constexpr float kF16Max = 65504.0f;  // a sum of P above it: some P may have overflowed in fp16
+constexpr int kMaxCtas = 160;        // partial slots are sized for this many CTAs
 constexpr int kSeqSlots = 4;
-constexpr int kSeqConsumers = 11;  // every warp but the producer
+constexpr int kSeqConsumers = 12;  // every warp but the planning one, the issuer twice (S and PV)
 
 constexpr int kSiteProducer = 1, kSiteIssuer = 2, kSiteSoftmax = 3, kSiteConvert = 4, kSiteQuery = 5;
 constexpr int kSiteInput = 100;  // lengths or page numbers that do not fit
 
-template <int D>
+// PAIR: an item is two row tiles, which share its K and V tiles.
+template <int D, bool PAIR>
 struct Cfg {
   static constexpr int kTileBytes = BN * D * 2;
   static constexpr int kColBlockBytes = BN * 128;
-  // slots of the K and of the V ring: 160 or 192 KB in flight.  S runs a step ahead of PV, so K is
-  // needed earlier and held shorter
+  static constexpr int kQ = PAIR ? 2 : 1;  // row tiles of an item
+  // slots of the K and of the V ring: with Q some 224 KB in all
   static constexpr int kK = D == 128 ? 3 : 6;
-  static constexpr int kV = D == 128 ? 2 : 6;
-  static constexpr int kSmemBytes = (2 + kK + kV) * kTileBytes + 1024;
+  static constexpr int kV = (D == 128 ? 7 : 14) - kQ - kK;
+  static constexpr int kSmemBytes = (kQ + kK + kV) * kTileBytes + 1024;
+  // registers per thread of the three warpgroups
+  static constexpr uint32_t kRegsSoftmax = PAIR ? 200 : 232;
+  static constexpr uint32_t kRegsConvert = PAIR ? 200 : 136;  // pair: the second row tile's softmax
+  static constexpr uint32_t kRegsOther = PAIR ? 104 : 136;
+  static constexpr int kConvertWarps = PAIR ? 8 : 4;
+  static_assert(128 * (kRegsSoftmax + kRegsConvert + kRegsOther) <= kThreads * kRegsLaunch, "register split");
+  // P of step q has TMEM columns of its own, or takes the first columns of its S
+  static constexpr bool kOverS = PAIR && D == 128;
+  static_assert(kTmemO + kQ * D <= (kOverS ? kTmemCols : kTmemP), "O and P in columns of their own");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
 struct Params {
-  const __nv_bfloat16* q;
-  int64_t q_token, q_head;
   __nv_bfloat16* o;
   float* lse;
   const int32_t* cu;
@@ -94,15 +120,28 @@ struct Params {
   int mask_words;
   int rows, max_pages, n_pages, page_size;  // rows: sequences
   int n_tokens, Hq, Hkv, G;
-  int R;  // tokens per item: BM / G
+  int R;  // tokens per row tile: BM / G
+  int item_tokens;  // R, or 2 R where an item is a pair of row tiles
+  uint32_t G_inv;  // ceil(2^16 / G): r / G = r * G_inv >> 16 for the rows r < 256 of an item
   int window, sinks;
   float c;  // scale * log2(e)
-  float* part_o;    // [kMaxCtas][2][BM][D]
-  float* part_lse;  // [kMaxCtas][2][BM], log2 units
-  int4* desc;       // [kMaxCtas]: the split item that CTA c begins: {rows, first token, kv head, last CTA}; rows 0: none
+  float* part_o;    // [kMaxCtas][2][2 BM][D]
+  float* part_lse;  // [kMaxCtas][2][2 BM], log2 units
+  int4* desc;       // [kMaxCtas]: the split item that CTA c begins: {tokens, first token, kv head, last CTA}; 0: none
+};
+
+// q as [token][kv head][head of the group][D], in boxes of as many tokens as 128, 64 or 32 rows hold.
+struct QMaps {
+  CUtensorMap rows128, rows64, rows32;
 };
 
 __device__ int g_paged_status;
+
+// a / b for 0 <= a, 0 < b, in 32 bits where they fit (a division in 64 takes some 500 cycles).
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
 
 // One sequence's queries and keys.
 struct Seq {
@@ -130,7 +169,7 @@ __device__ __forceinline__ Seq seq_at(const Params& p, int b, bool& bad) {
   return s;
 }
 
-// The key tiles that row tile rt of a sequence visits: the first n_sink, then from j0 on.
+// The key tiles that item rt of a sequence visits: the first n_sink, then from j0 on.
 struct Tiles {
   int steps, n_sink, j0;
 };
@@ -138,8 +177,8 @@ struct Tiles {
 __device__ __forceinline__ Tiles tiles_of(const Params& p, const Seq& s, int rt) {
   Tiles t{1, 0, 0};  // a sequence without keys visits one tile, all of it masked
   if (s.kv_len == 0) return t;
-  const int first = rt * p.R;
-  const int hi = p.mask ? s.kv_len : s.ctx + min(first + p.R, s.n);
+  const int first = rt * p.item_tokens;
+  const int hi = p.mask ? s.kv_len : s.ctx + min(first + p.item_tokens, s.n);
   const int n_hi = (hi + BN - 1) / BN;
   if (p.window > 0) {
     // no row's window begins earlier (a drafted token that sees none is at ctx - 1)
@@ -151,8 +190,14 @@ __device__ __forceinline__ Tiles tiles_of(const Params& p, const Seq& s, int rt)
   return t;
 }
 
+// Token of row r of an item (r < 256: r * G < 2^16, so the product is exact enough).
+__device__ __forceinline__ int token_of(const Params& p, int r) {
+  return static_cast<int>(static_cast<uint32_t>(r) * p.G_inv >> 16);
+}
+
 // What a CTA does of one (row tile, kv head): steps [s0, s1) of its tiles.
 struct Item {
+  int b;            // sequence
   int tok0;         // first query token (into q)
   int first, ntok;  // ... its place among the sequence's newest tokens; tokens of the item
   int h;            // kv head
@@ -162,17 +207,34 @@ struct Item {
   int seq_n;  // the sequence's newest tokens
   int out;    // where the result goes: 0 O and LSE, 1 the CTA's first partial, 2 its second
   __device__ __forceinline__ int tile(int s) const { return s < n_sink ? s : j0 + s - n_sink; }
+  // Key groups (see the kernel's head): how many times the rows are repeated.
+  __device__ __forceinline__ int groups(int G) const {
+    const int rows = ntok * G;
+    return rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+  }
+  // Row tiles: 1, or 2 that take each key tile in turn.
+  __device__ __forceinline__ int row_tiles(int R) const { return ntok > R ? 2 : 1; }
 };
-constexpr int kItemWords = 12;
+constexpr int kItemWords = 13;
 static_assert(sizeof(Item) == 4 * kItemWords, "published word by word");
 
 __device__ __forceinline__ uint8_t* align_1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~static_cast<uintptr_t>(1023));
 }
 
+// Every lane polls; the answer is made warp-uniform.  A loop of few instructions, the clock read
+// only after a poll has failed: most of this kernel's warps wait most of the time, beside warps that need
+// the issue slots and the instruction cache (64 sequences of up to 8192 keys: 335 us with
+// mbar_wait_bounded, 293 with this).
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag,
                                           uint64_t timeout_ns) {
-  const bool ok = mbar_wait_bounded(bar, parity, abort_flag, timeout_ns);
+  uint64_t t0 = 0;
+  bool ok;
+  while (!(ok = mbar_try_wait(bar, parity))) {
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (*abort_flag || now - t0 > timeout_ns) break;
+  }
   return __all_sync(0xffffffffu, ok);
 }
 
@@ -190,6 +252,19 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, u
       : "memory");
 }
 
+// Whether the phase with the given parity has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Bits [lo, hi) of a 32-bit word whose first bit stands for `base`.
 __device__ __forceinline__ uint32_t range_bits(int base, int lo, int hi) {
   const int a = max(lo - base, 0), b = min(hi - base, 32);
@@ -197,30 +272,67 @@ __device__ __forceinline__ uint32_t range_bits(int base, int lo, int hi) {
   return (0xFFFFFFFFu >> (32 - (b - a))) << a;
 }
 
+// The greater of each half; NaN where either is.
+__device__ __forceinline__ uint32_t max_nan_f16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // A NaN in either half of a pair of fp16?
 __device__ __forceinline__ bool has_nan_f16x2(uint32_t w) {
   return (w & 0x7FFFu) > 0x7C00u || ((w >> 16) & 0x7FFFu) > 0x7C00u;
 }
 
-template <int D>
+// 16 consecutive TMEM columns of this warp's lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Both halves of a pair of fp16 times a.
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t w, float a) {
+  const uint32_t a2 = pack_f16x2(a, a);
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(w), "r"(a2));
+  return d;
+}
+
+template <int D, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tree_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const Params p) {
-  using C = Cfg<D>;
+    attn_tree_kernel(const __grid_constant__ QMaps tq, const __grid_constant__ CUtensorMap tk,
+                     const __grid_constant__ CUtensorMap tv, const Params p) {
+  using C = Cfg<D, PAIR>;
   constexpr int KS = C::kK, VS = C::kV;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_1024(smem_raw);
-  uint8_t* q_s = smem;                      // two Q buffers
-  uint8_t* k_s = smem + 2 * C::kTileBytes;
+  uint8_t* q_s = smem;
+  uint8_t* k_s = smem + C::kQ * C::kTileBytes;
   uint8_t* v_s = k_s + KS * C::kTileBytes;
   __shared__ uint64_t k_full[KS], k_empty[KS], v_full[VS], v_empty[VS];
-  __shared__ uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done, o_full, o_empty, mma_drain;
+  __shared__ uint64_t q_full, q_empty, s_full[2], p_full[2], pv_done, o_full[2], o_empty[2], joined, mma_drain;
   __shared__ uint64_t seq_full[kSeqSlots], seq_empty[kSeqSlots];
   __shared__ int item_words[kSeqSlots][kItemWords];
   // Step g's V tile has been converted, and which of its keys hold a NaN, at g % kReady.  A softmax
-  // warp looks at them after handing over P(g), when the conversion may be up to VS steps ahead;
-  // with more places than that neither is reused under it.
-  constexpr int kReady = 8;
-  static_assert(VS < kReady, "read before it is used again");
+  // warp at step g looks at the keys of step g - 2, when the conversion may be at step g - 1 + VS;
+  // with more places than lie between neither is reused under it.
+  constexpr int kReady = 16;
+  static_assert(VS + 2 < kReady, "read before it is used again");
   __shared__ uint64_t v_ready[kReady];
   __shared__ __align__(16) uint32_t nan_keys[kReady][4];
   __shared__ uint32_t tmem_base_slot, abort_flag;
@@ -238,16 +350,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    for (int s = 0; s < kReady; ++s) mbar_init(&v_ready[s], 4);  // one arrival per converting warp
+    for (int s = 0; s < kReady; ++s) mbar_init(&v_ready[s], C::kConvertWarps);
+    mbar_init(&q_full, 1);
+    mbar_init(&q_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&q_full[i], 2);
-      mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 128);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_full[i], 1);
+      mbar_init(&o_empty[i], 128);
     }
     mbar_init(&pv_done, 1);
-    mbar_init(&o_full, 1);
-    mbar_init(&o_empty, 128);
+    mbar_init(&joined, 4);
     mbar_init(&mma_drain, 1);
     for (int i = 0; i < kSeqSlots; ++i) {
       mbar_init(&seq_full[i], 1);
@@ -255,6 +368,65 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     abort_flag = 0;
     fence_mbar_init();
+  }
+  // The planning warp's place in the list of key tiles, found while the others set up.
+  int64_t per = 0, at = 0, end = 0;  // key tiles per CTA; this CTA's part of the list: [at, end)
+  int b = 0, rt = 0, h = 0, s0 = 0;  // ... where it begins: sequence, item of it, kv head, step
+  Seq seq{0, 0, 0, 0};
+  Tiles t{1, 0, 0};
+  bool bad = false;
+  if (warp == kKeyWarp) {
+    // key tiles of sequence b, over its row tiles and kv heads
+    auto weight = [&](const Seq& s) {
+      int64_t w = 0;
+      for (int rt = 0; rt * p.item_tokens < s.n; ++rt) w += tiles_of(p, s, rt).steps;
+      return w * p.Hkv;
+    };
+    const Seq seq_first = seq_at(p, lane, bad);  // the first 32 sequences stay in registers
+    const int64_t w_first = weight(seq_first);
+    int64_t total = w_first;
+    for (int i = 32 + lane; i < p.rows; i += 32) total += weight(seq_at(p, i, bad));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    per = divide(total + gridDim.x - 1, gridDim.x);
+    at = per * blockIdx.x;
+    end = min(at + per, total);
+    if (at < end) {
+      // the sequence that holds `at`, then the row tile, the kv head and the step
+      int64_t before = 0;
+      for (int base = 0; base < p.rows; base += 32) {
+        const Seq mine = base == 0 ? seq_first : seq_at(p, base + lane, bad);
+        const int64_t w = base == 0 ? w_first : weight(mine);
+        int64_t incl = w;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+          if (lane >= d) incl += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, before + incl > at);
+        if (past) {
+          const int l = __ffs(past) - 1;
+          b = base + l;
+          before += __shfl_sync(0xffffffffu, incl - w, l);
+          seq.c0 = __shfl_sync(0xffffffffu, mine.c0, l);
+          seq.n = __shfl_sync(0xffffffffu, mine.n, l);
+          seq.ctx = __shfl_sync(0xffffffffu, mine.ctx, l);
+          seq.kv_len = __shfl_sync(0xffffffffu, mine.kv_len, l);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+      }
+      int64_t rem = at - before;
+      for (; rt * p.item_tokens < seq.n; ++rt) {
+        t = tiles_of(p, seq, rt);
+        const int64_t here = static_cast<int64_t>(t.steps) * p.Hkv;
+        if (rem < here) break;
+        rem -= here;
+      }
+      h = static_cast<int>(divide(rem, t.steps));
+      s0 = static_cast<int>(rem - static_cast<int64_t>(h) * t.steps);
+      if (rt * p.item_tokens >= seq.n || h >= p.Hkv) at = end;  // the lengths changed under the call
+    }
   }
   if (warp == kMmaWarp) {
     tmem_alloc(&tmem_base_slot, kTmemCols);
@@ -277,150 +449,178 @@ __global__ void __launch_bounds__(kThreads, 1)
     return true;
   };
 
+  // Loads the pages of an item's key tiles, step by step, through a ring of tile slots (both TMA
+  // warps; `n` counts the loads of the launch).  Lane i of the window of 32 page numbers that the
+  // warp holds loads page i.
+  const int per_tile = p.page_size >= BN ? 1 : BN / p.page_size;  // pages of a tile
+  const int box_rows = min(p.page_size, BN);
+  auto stream = [&](const Item& item, const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty,
+                    uint32_t slots, uint32_t& n) -> bool {
+    const int32_t* row = p.table + static_cast<int64_t>(item.b) * p.max_pages;
+    const int used = (item.kv_len + p.page_size - 1) / p.page_size;
+    auto load_ids = [&](int w) { return w + lane < used ? __ldg(row + w + lane) : 0; };
+    int win = -64, ids = 0, ids_next = 0;  // pages [win, win + 32) of the row, and the next 32 on their way
+    for (int s = item.s0; s < item.s1; ++s, ++n) {
+      const int key0 = item.tile(s) * BN;
+      const int page0 = key0 / p.page_size, slot0 = key0 % p.page_size;
+      if (page0 / 32 * 32 != win) {
+        const int w = page0 / 32 * 32;
+        ids = w == win + 32 ? ids_next : load_ids(w);
+        ids_next = load_ids(w + 32);
+        win = w;
+      }
+      // lane page0 - win + i loads the tile's page i, if the sequence reaches it
+      const int i = lane - (page0 - win);
+      const bool mine = i >= 0 && i < per_tile && key0 + i * box_rows < item.kv_len;
+      int page = ids;
+      if (mine && (page < 0 || page >= p.n_pages)) {
+        atomicCAS(&g_paged_status, 0, kSiteInput);
+        page = max(p.n_pages, 1);  // past the pool: reads as zeros
+      }
+      const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * static_cast<uint32_t>(box_rows * D * 2);
+      const uint32_t slot = n % slots;
+      if (n >= slots && !warp_wait(&empty[slot], (n / slots - 1) & 1, abort_v, kTimeoutNs)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], bytes);
+      __syncwarp();
+      if (mine) {
+#pragma unroll
+        for (int cb = 0; cb < D / 64; ++cb)
+          tma_load_4d(ring + slot * C::kTileBytes + cb * C::kColBlockBytes + i * box_rows * 128, map, &full[slot],
+                      cb * 64, slot0, item.h, page);
+      }
+      __syncwarp();
+    }
+    return true;
+  };
+  // unwinding: let the copies in flight land before the CTA exits
+  auto drain = [&](uint64_t* full, uint32_t slots, uint32_t n) {
+    for (uint32_t i = (n > slots ? n - slots : 0); i < n; ++i)
+      mbar_wait_bounded(&full[i % slots], (i / slots) & 1, abort_v, kDrainTimeoutNs);
+  };
+
+  // V of step s (step g of the launch) from bf16 to fp16 in its slot, the share of converting warp w:
+  // kShare rows, a lane's 16-byte chunk holding 8 values of one row.  Rows past the sequence become 0,
+  // whatever the page holds.  So does the V row of a key that holds a NaN, and the key is noted: the
+  // rows that see it get NaN in the epilogue, a row that does not is not reached through 0 * NaN.
+  auto convert = [&](const Item& item, int s, uint32_t g, int w) -> bool {
+    constexpr int kShare = BN / C::kConvertWarps, kPieces = kShare / 4 * (D / 64);  // chunks per lane
+    const uint32_t slot = g % VS;
+    if (!warp_wait(&v_full[slot], (g / VS) & 1, abort_v, kTimeoutNs)) return false;
+    const int valid = item.kv_len - item.tile(s) * BN - kShare * w;  // rows of the share that are tokens
+    const uint32_t base = smem_u32(v_s + slot * C::kTileBytes) + w * kShare * 128 + lane * 16;
+    auto chunk = [&](int u) { return base + (u / (kShare / 4)) * C::kColBlockBytes + (u % (kShare / 4)) * 512; };
+    uint32_t top = 0xFC00FC00u;  // NaN if any value is
+    // four chunks at a time, rolled: the code of the warps that share the SM's instruction cache stays
+    // small
+#pragma unroll 1
+    for (int u = 0; u < kPieces; u += 4) {
+      const uint32_t at = chunk(u);
+      uint4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = lds128(at + i * 512);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i].x = bf16x2_to_f16x2(x[i].x);
+        x[i].y = bf16x2_to_f16x2(x[i].y);
+        x[i].z = bf16x2_to_f16x2(x[i].z);
+        x[i].w = bf16x2_to_f16x2(x[i].w);
+      }
+      if (valid < kShare) {  // the sequence ends in the share
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (4 * ((u + i) % (kShare / 4)) + lane / 8 >= valid) x[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        top = max_nan_f16x2(top, max_nan_f16x2(max_nan_f16x2(x[i].x, x[i].y), max_nan_f16x2(x[i].z, x[i].w)));
+        sts128(at + i * 512, x[i]);
+      }
+    }
+    uint32_t keys = 0;
+    if (__any_sync(0xffffffffu, has_nan_f16x2(top))) {  // rare: find the keys, then clear their rows
+      for (int pass = 0; pass < 2; ++pass)
+#pragma unroll 1
+        for (int u = 0; u < kPieces; ++u) {
+          const uint4 y = lds128(chunk(u));
+          const bool nan = has_nan_f16x2(y.x) || has_nan_f16x2(y.y) || has_nan_f16x2(y.z) || has_nan_f16x2(y.w);
+          const uint32_t hit = __ballot_sync(0xffffffffu, nan);
+          const int r = 4 * (u % (kShare / 4));
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((hit >> (8 * i)) & 0xFFu) keys |= 1u << (r + i);
+          if (pass == 1 && ((keys >> (r + lane / 8)) & 1u)) sts128(chunk(u), make_uint4(0u, 0u, 0u, 0u));
+        }
+    }
+    if (lane == 0) {
+      if constexpr (kShare == 32)
+        nan_keys[g % kReady][w] = keys;
+      else
+        reinterpret_cast<uint16_t*>(nan_keys[g % kReady])[w] = static_cast<uint16_t>(keys);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&v_ready[g % kReady]);
+    return true;
+  };
+
   if (warp >= 8) {
-    regs_decrease<kRegsOther>();
-    if (warp == kLoadWarp) {
-      // ------------------------------------------------------------ plan, then TMA producer
-      if (lane == 0) {
-        tma_prefetch_map(&tk);
-        tma_prefetch_map(&tv);
-      }
-      bool bad = false;
-      // key tiles of sequence b, over its row tiles and kv heads
-      auto weight = [&](int b) {
-        const Seq s = seq_at(p, b, bad);
-        int64_t w = 0;
-        for (int rt = 0; rt * p.R < s.n; ++rt) w += tiles_of(p, s, rt).steps;
-        return w * p.Hkv;
-      };
-      const int64_t w_first = weight(lane);  // the first 32 sequences' stay in registers
-      int64_t total = w_first;
-      for (int b = 32 + lane; b < p.rows; b += 32) total += weight(b);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-      const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-      int64_t at = per * blockIdx.x;  // this CTA's part of the list: [at, end)
-      const int64_t end = min(at + per, total);
-      int b = 0, rt = 0, h = 0, s0 = 0;
-      Seq seq{0, 0, 0, 0};
-      Tiles t{1, 0, 0};
-      if (at < end) {
-        // the sequence that holds `at`, then the row tile, the kv head and the step
-        int64_t before = 0;
-        for (int base = 0; base < p.rows; base += 32) {
-          const int64_t w = base == 0 ? w_first : weight(base + lane);
-          int64_t incl = w;
-#pragma unroll
-          for (int d = 1; d < 32; d *= 2) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-          }
-          const uint32_t past = __ballot_sync(0xffffffffu, before + incl > at);
-          if (past) {
-            const int l = __ffs(past) - 1;
-            b = base + l;
-            before += __shfl_sync(0xffffffffu, incl - w, l);
-            break;
-          }
-          before += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        seq = seq_at(p, b, bad);
-        int64_t rem = at - before;
-        for (; rt * p.R < seq.n; ++rt) {
-          t = tiles_of(p, seq, rt);
-          const int64_t here = static_cast<int64_t>(t.steps) * p.Hkv;
-          if (rem < here) break;
-          rem -= here;
-        }
-        h = static_cast<int>(rem / t.steps);
-        s0 = static_cast<int>(rem % t.steps);
-        if (rt * p.R >= seq.n || h >= p.Hkv) at = end;  // the lengths changed under the call
-      }
+    regs_decrease<C::kRegsOther>();
+    if (warp == kKeyWarp || warp == kValueWarp) {
+      // ------------------------------------------------------------ K or V pages; warp 8 plans
+      const bool keys = warp == kKeyWarp;
+      const CUtensorMap* map = keys ? &tk : &tv;
+      uint64_t* full = keys ? k_full : v_full;
+      uint64_t* empty = keys ? k_empty : v_empty;
+      const uint32_t slots = keys ? KS : VS;
+      if (lane == 0) tma_prefetch_map(map);
       if (bad) atomicCAS(&g_paged_status, 0, kSiteInput);
       int4 desc = make_int4(0, 0, 0, 0);
-      uint32_t g = 0, v_loads = 0;  // steps whose K, and whose V, is on its way
+      uint32_t n_loads = 0;
       bool ok = true;
-      const int per_tile = p.page_size >= BN ? 1 : BN / p.page_size;  // pages of a tile
-      const int box_rows = min(p.page_size, BN);
       for (int k = 0; ok; ++k) {
         Item item;
-        const bool more = at < end;
-        item.s0 = s0;
-        item.s1 = more ? static_cast<int>(min(static_cast<int64_t>(t.steps), s0 + (end - at))) : 0;
-        item.first = rt * p.R;
-        item.ntok = min(p.R, seq.n - item.first);
-        item.tok0 = seq.c0 + item.first;
-        item.h = h;
-        item.n_sink = t.n_sink;
-        item.j0 = t.j0;
-        item.ctx = seq.ctx;
-        item.kv_len = seq.kv_len;
-        item.seq_n = seq.n;
-        item.out = item.s0 == 0 && item.s1 == t.steps ? 0 : item.s0 == 0 ? 2 : 1;
-        if (k >= kSeqSlots) ok = warp_wait(&seq_empty[k % kSeqSlots], (k / kSeqSlots - 1) & 1, abort_v, kTimeoutNs);
-        if (!ok) break;
-        if (lane == 0) {
-          const int* src = reinterpret_cast<const int*>(&item);
-#pragma unroll
-          for (int i = 0; i < kItemWords; ++i) item_words[k % kSeqSlots][i] = src[i];
-          mbar_arrive(&seq_full[k % kSeqSlots]);
-        }
-        __syncwarp();
-        if (!more) break;
-        if (item.out == 2) {  // the CTAs after this one hold the rest of the item
-          const int64_t last = at - s0 + t.steps - 1;
-          desc = make_int4(item.ntok * p.G, item.tok0, h, static_cast<int>(last / per));
-        }
-        // pages [win, win + 32) of the row, one per lane, and the next 32 on their way
-        const int32_t* row = p.table + static_cast<int64_t>(b) * p.max_pages;
-        const int used = (item.kv_len + p.page_size - 1) / p.page_size;
-        auto load_ids = [&](int w) { return w + lane < used ? __ldg(row + w + lane) : 0; };
-        int win = -64, ids = 0, ids_next = 0;
-        for (int s = item.s0; s < item.s1 && ok; ++s) {
-          const int key0 = item.tile(s) * BN;
-          const int page0 = key0 / p.page_size, slot0 = key0 % p.page_size;
-          if (page0 / 32 * 32 != win) {
-            const int w = page0 / 32 * 32;
-            ids = w == win + 32 ? ids_next : load_ids(w);
-            ids_next = load_ids(w + 32);
-            win = w;
-          }
-          // lane page0 - win + i loads the tile's page i, if the sequence reaches it
-          const int i = lane - (page0 - win);
-          const bool mine = i >= 0 && i < per_tile && key0 + i * box_rows < item.kv_len;
-          int page = ids;
-          if (mine && (page < 0 || page >= p.n_pages)) {
-            atomicCAS(&g_paged_status, 0, kSiteInput);
-            page = max(p.n_pages, 1);  // past the pool: reads as zeros
-          }
-          const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * static_cast<uint32_t>(box_rows * D * 2);
-          // the page's slots into ring slot `slot` of K or V
-          auto load = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* full) {
-            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-            __syncwarp();
-            if (mine) {
-#pragma unroll
-              for (int cb = 0; cb < D / 64; ++cb)
-                tma_load_4d(dst + cb * C::kColBlockBytes + i * box_rows * 128, map, full, cb * 64, slot0, h, page);
-            }
-            __syncwarp();
-          };
-          if (g >= KS) ok = warp_wait(&k_empty[g % KS], (g / KS - 1) & 1, abort_v, kTimeoutNs);
+        if (!keys) {
+          ok = next_item(k, item);
+          if (!ok || item.s1 == 0) break;
+        } else {
+          const bool more = at < end;
+          item.b = b;
+          item.s0 = s0;
+          item.s1 = more ? static_cast<int>(min(static_cast<int64_t>(t.steps), s0 + (end - at))) : 0;
+          item.first = rt * p.item_tokens;
+          item.ntok = min(p.item_tokens, seq.n - item.first);
+          item.tok0 = seq.c0 + item.first;
+          item.h = h;
+          item.n_sink = t.n_sink;
+          item.j0 = t.j0;
+          item.ctx = seq.ctx;
+          item.kv_len = seq.kv_len;
+          item.seq_n = seq.n;
+          item.out = item.s0 == 0 && item.s1 == t.steps ? 0 : item.s0 == 0 ? 2 : 1;
+          if (k >= kSeqSlots) ok = warp_wait(&seq_empty[k % kSeqSlots], (k / kSeqSlots - 1) & 1, abort_v, kTimeoutNs);
           if (!ok) break;
-          load(&tk, k_s + (g % KS) * C::kTileBytes, &k_full[g % KS]);
-          ++g;
-          if (v_loads >= VS) ok = warp_wait(&v_empty[v_loads % VS], (v_loads / VS - 1) & 1, abort_v, kTimeoutNs);
-          if (!ok) break;
-          load(&tv, v_s + (v_loads % VS) * C::kTileBytes, &v_full[v_loads % VS]);
-          ++v_loads;
+          if (lane == 0) {
+            const int* src = reinterpret_cast<const int*>(&item);
+#pragma unroll
+            for (int i = 0; i < kItemWords; ++i) item_words[k % kSeqSlots][i] = src[i];
+            mbar_arrive(&seq_full[k % kSeqSlots]);
+          }
+          __syncwarp();
+          if (!more) break;
+          if (item.out == 2) {  // the CTAs after this one hold the rest of the item
+            const int64_t last = at - s0 + t.steps - 1;
+            desc = make_int4(item.ntok, item.tok0, h, static_cast<int>(divide(last, per)));
+          }
         }
+        ok = stream(item, map, keys ? k_s : v_s, full, empty, slots, n_loads);
+        if (!keys) continue;
         // the next (row tile, kv head)
         at += item.s1 - item.s0;
         s0 = 0;
         if (at < end && ++h == p.Hkv) {
           h = 0;
           ++rt;
-          if (rt * p.R >= seq.n) {
+          if (rt * p.item_tokens >= seq.n) {
             rt = 0;
             do {
               seq = seq_at(p, ++b, bad);
@@ -432,379 +632,552 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) {
         if (lane == 0) record_abort(abort_v, kSiteProducer);
         desc = make_int4(0, 0, 0, 0);
-        // unwinding: let the copies in flight land before the CTA exits
-        for (uint32_t i = (g > KS ? g - KS : 0); i < g; ++i)
-          mbar_wait_bounded(&k_full[i % KS], (i / KS) & 1, abort_v, kDrainTimeoutNs);
-        for (uint32_t i = (v_loads > VS ? v_loads - VS : 0); i < v_loads; ++i)
-          mbar_wait_bounded(&v_full[i % VS], (i / VS) & 1, abort_v, kDrainTimeoutNs);
+        drain(full, slots, n_loads);
       }
-      if (lane == 0) p.desc[blockIdx.x] = desc;
+      if (keys && lane == 0) p.desc[blockIdx.x] = desc;
     } else if (warp == kMmaWarp) {
       // ------------------------------------------------------------ tcgen05 issuer
+      // Products q = 0, 1, ..: a step's row tiles in turn, steps and items in order.  S(q) and P(q)
+      // lie in TMEM region q & 1.  S runs two products ahead of PV:
+      //   S(0) S(1) | PV(0) S(2) | PV(1) S(3) | ...
       constexpr uint32_t idesc_s = idesc_bf16_f32(BM, BN, false);
       constexpr uint32_t idesc_pv = idesc_f16_f32(BM, D, true);
       const uint32_t q_addr = smem_u32(q_s), k_addr = smem_u32(k_s), v_addr = smem_u32(v_s);
       static_assert(C::kColBlockBytes == 16384, "K-step offsets of mma_bf16_ss_k8");
-      // S of step g from Q buffer qb
-      auto issue_s = [&](uint32_t g, uint32_t qb) {
-        const uint32_t slot = g % KS;
-        const uint64_t qd = sdesc_sw128(opaque(q_addr) + qb * C::kTileBytes, 16, 1024);
-        const uint64_t kd = sdesc_sw128(opaque(k_addr) + slot * C::kTileBytes, 16, 1024);
-        if constexpr (D == 128)
-          mma_bf16_ss_k8(tmem + (g & 1) * BN, qd, kd, idesc_s, smem_u32(&s_full[g & 1]), smem_u32(&k_empty[slot]));
-        else
-          mma_bf16_ss_k4(tmem + (g & 1) * BN, qd, kd, idesc_s, smem_u32(&s_full[g & 1]), smem_u32(&k_empty[slot]));
+      bool ok = true;
+      // where a walk over the products is: item k, its step s and row tile t, key tile n of the launch
+      struct Walk {
+        Item item;
+        int k, s, t, tiles;
+        uint32_t q, n;
       };
-      auto issue_pv = [&](uint32_t g, bool accumulate) {
-        const uint32_t slot = g % VS;
-        const uint64_t vd = sdesc_sw128(opaque(v_addr) + slot * C::kTileBytes, C::kColBlockBytes, 1024);
-        mma_bf16_ts_k8(tmem + kTmemO, tmem + (g & 1) * BN + 64, vd, idesc_pv, accumulate ? 1u : 0u,
-                       smem_u32(&pv_done), smem_u32(&v_empty[slot]));
+      auto enter = [&](Walk& w) {  // the walk's next item has been published; none: item.s1 == 0
+        next_item(++w.k, w.item);
+        w.s = w.item.s0;
+        w.t = 0;
+        w.tiles = PAIR ? w.item.row_tiles(p.R) : 1;
       };
-      auto wait_k = [&](uint32_t n) { return warp_wait(&k_full[n % KS], (n / KS) & 1, abort_v, kTimeoutNs); };
-      // first S of item k (steps from g on)
-      auto begin = [&](int k, uint32_t g) {
-        if (!warp_wait(&q_full[k & 1], (k >> 1) & 1, abort_v, kTimeoutNs) || !wait_k(g)) return false;
-        tc_fence_after();
-        issue_s(g, k & 1);
-        return true;
+      auto advance = [&](Walk& w) {
+        ++w.q;
+        if (++w.t < w.tiles) return;
+        w.t = 0;
+        ++w.n;
+        ++w.s;
       };
-      uint32_t g = 0;
-      Item item;
-      bool ok = next_item(0, item);
-      if (ok && item.s1 > 0) {
-        ok = begin(0, 0);
-        if (ok && item.s1 - item.s0 == 1) mma_commit_elect(&q_empty[0]);
-      }
-      for (int k = 0; ok && item.s1 > 0; ++k) {
-        const int n = item.s1 - item.s0;
-        Item next;
-        next.s0 = next.s1 = 0;
-        for (int j = 0; j < n && ok; ++j, ++g) {
-          // S of the next step: this item's, or the next item's first
-          if (j + 1 < n) {
-            ok = wait_k(g + 1);
-            if (!ok) break;
+      auto is_done = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_test(bar, parity)); };
+      // the walk is between items: whether the next one is there
+      auto next_is_out = [&](const Walk& w) {
+        return is_done(&seq_full[(w.k + 1) % kSeqSlots], ((w.k + 1) / kSeqSlots) & 1);
+      };
+      Walk a, b;  // S, PV
+      a.k = b.k = -1;
+      a.q = b.q = a.n = b.n = 0;
+      a.item.s1 = b.item.s1 = a.s = b.s = 1;
+      uint32_t n_out[2] = {0, 0};  // items whose O went through each accumulator
+      uint64_t idle_since = 0;
+      // Whichever of the next S and the next PV has its operands is issued; neither waits for the other's.
+      while (b.item.s1 > 0) {
+        bool idle = true;
+        if (a.item.s1 > 0 && a.q < b.q + 2) {
+          if (a.s == a.item.s1 && next_is_out(a)) enter(a);
+          if (a.s < a.item.s1 && (a.t > 0 || ((a.s > a.item.s0 || is_done(&q_full, a.k & 1)) &&
+                                              is_done(&k_full[a.n % KS], (a.n / KS) & 1)))) {
             tc_fence_after();
-            issue_s(g + 1, k & 1);
-            if (j + 2 == n) mma_commit_elect(&q_empty[k & 1]);  // the item's last S has been issued
-          } else {
-            ok = next_item(k + 1, next);
-            if (ok && next.s1 > 0) {
-              ok = begin(k + 1, g + 1);
-              if (ok && next.s1 - next.s0 == 1) mma_commit_elect(&q_empty[(k + 1) & 1]);
-            }
-            if (!ok) break;
+            const uint32_t slot = a.n % KS;
+            const uint64_t qd = sdesc_sw128(opaque(q_addr) + a.t * C::kTileBytes, 16, 1024);
+            const uint64_t kd = sdesc_sw128(opaque(k_addr) + slot * C::kTileBytes, 16, 1024);
+            const uint32_t free_k = a.t + 1 == a.tiles ? smem_u32(&k_empty[slot]) : kNoBar;
+            if constexpr (D == 128)
+              mma_bf16_ss_k8(tmem + (a.q & 1) * BN, qd, kd, idesc_s, smem_u32(&s_full[a.q & 1]), free_k);
+            else
+              mma_bf16_ss_k4(tmem + (a.q & 1) * BN, qd, kd, idesc_s, smem_u32(&s_full[a.q & 1]), free_k);
+            if (a.t + 1 == a.tiles && a.s + 1 == a.item.s1) mma_commit_elect(&q_empty);  // the item's last S
+            advance(a);
+            idle = false;
           }
-          ok = warp_wait(&v_ready[g % kReady], (g / kReady) & 1, abort_v, kTimeoutNs);
-          if (ok && j == 0 && k > 0) ok = warp_wait(&o_empty, (k - 1) & 1, abort_v, kTimeoutNs);
-          if (ok) ok = warp_wait(&p_full[g & 1], (g >> 1) & 1, abort_v, kTimeoutNs);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(g, j > 0);
-          if (j + 1 == n) mma_commit_elect(&o_full);  // the item's O is complete
         }
-        item = next;
+        if (b.s == b.item.s1 && next_is_out(b)) enter(b);
+        if (b.s < b.item.s1 && b.q < a.q && is_done(&p_full[b.q & 1], (b.q >> 1) & 1) &&
+            (b.t > 0 || is_done(&v_ready[b.n % kReady], (b.n / kReady) & 1))) {
+          const bool first = b.s == b.item.s0, last = b.s + 1 == b.item.s1;
+          const uint32_t outs = b.t == 0 ? n_out[0] : n_out[1];
+          if (!first || outs == 0 || is_done(&o_empty[b.t], (outs - 1) & 1)) {
+            tc_fence_after();
+            const uint32_t slot = b.n % VS;
+            const uint64_t vd = sdesc_sw128(opaque(v_addr) + slot * C::kTileBytes, C::kColBlockBytes, 1024);
+            // with key groups the epilogue uses the last V slot as its stage and hands it back itself
+            const bool keep = b.t + 1 < b.tiles || (last && b.item.groups(p.G) > 1);
+            mma_bf16_ts_k8(tmem + kTmemO + b.t * D,
+                           tmem + (C::kOverS ? (b.q & 1) * BN : kTmemP + (b.q & 1) * (BN / 2)), vd, idesc_pv,
+                           first ? 0u : 1u, smem_u32(&pv_done), keep ? kNoBar : smem_u32(&v_empty[slot]));
+            if (last) {
+              mma_commit_elect(&o_full[b.t]);  // the row tile's O is complete
+              if (b.t == 0)
+                ++n_out[0];
+              else
+                ++n_out[1];
+            }
+            advance(b);
+            idle = false;
+          }
+        }
+        if (!idle) {
+          idle_since = 0;
+          continue;
+        }
+        const uint64_t now = global_timer_ns();
+        if (idle_since == 0) idle_since = now;
+        if (__any_sync(0xffffffffu, *abort_v || now - idle_since > kTimeoutNs)) {
+          ok = false;
+          break;
+        }
       }
       if (!ok && lane == 0) record_abort(abort_v, kSiteIssuer);
       mma_commit_elect(&mma_drain);
       warp_wait(&mma_drain, 0, abort_v, ok ? kTimeoutNs : kDrainTimeoutNs);
     } else {
       // ------------------------------------------------------------ Q rows
-      // Row r = token * G + head of the group, stored as a 128-byte-swizzled K-major tile; rows
-      // past the item's keep what the buffer held (their S rows are not used).
-      constexpr int kChunks = D / 8, kUnroll = 8;
-      const int me = (warp - 10) * 32 + lane;
+      // Row r of a row tile = token * G + head of the group: one box of the map for the item's number
+      // of key groups (128, 64 or 32 rows at most), once per group.  The box may reach into the next
+      // sequence's tokens; those rows of S are not used.
       bool ok = true;
+      int n_items = 0;
       for (int k = 0; ok; ++k) {
         Item item;
         ok = next_item(k, item);
         if (!ok || item.s1 == 0) break;
-        if (k >= 2) ok = warp_wait(&q_empty[k & 1], (k / 2 - 1) & 1, abort_v, kTimeoutNs);
+        const int groups = item.groups(p.G), tiles = PAIR ? item.row_tiles(p.R) : 1;
+        const CUtensorMap* map = groups == 4 ? &tq.rows32 : groups == 2 ? &tq.rows64 : &tq.rows128;
+        if (k >= 1) ok = warp_wait(&q_empty, (k - 1) & 1, abort_v, kTimeoutNs);
         if (!ok) break;
-        uint8_t* dst = q_s + (k & 1) * C::kTileBytes;
-        const int pieces = item.ntok * p.G * kChunks;
-        for (int e0 = me; e0 < pieces; e0 += 64 * kUnroll) {
-          uint4 x[kUnroll];
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) {
-            const int e = e0 + 64 * u, r = e / kChunks, ch = e % kChunks;
-            if (e < pieces)
-              x[u] = __ldg(reinterpret_cast<const uint4*>(p.q + (item.tok0 + r / p.G) * p.q_token +
-                                                          (item.h * p.G + r % p.G) * p.q_head + ch * 8));
-          }
-#pragma unroll
-          for (int u = 0; u < kUnroll; ++u) {
-            const int e = e0 + 64 * u, r = e / kChunks, ch = e % kChunks;
-            if (e < pieces)
-              *reinterpret_cast<uint4*>(dst + (ch / 8) * C::kColBlockBytes + r * 128 +
-                                        (((ch % 8) ^ (r & 7)) << 4)) = x[u];
-          }
-        }
-        fence_proxy_async_smem();
+        const uint32_t box = BM / groups / p.G * p.G * D * 2;
+        if (lane == 0) mbar_arrive_expect_tx(&q_full, box * groups * tiles);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[k & 1]);
+        if (lane < groups * tiles) {  // one lane per copy
+          uint8_t* dst = q_s + (tiles > 1 ? lane * C::kTileBytes : lane * (BM / groups) * 128);
+#pragma unroll
+          for (int cb = 0; cb < D / 64; ++cb)
+            tma_load_4d(dst + cb * C::kColBlockBytes, map, &q_full, cb * 64, 0, item.h,
+                        item.tok0 + (tiles > 1 ? lane * p.R : 0));
+        }
+        __syncwarp();
+        n_items = k + 1;
       }
-      if (!ok && lane == 0) record_abort(abort_v, kSiteQuery);
+      if (!ok) {
+        if (lane == 0) record_abort(abort_v, kSiteQuery);
+        if (n_items > 0) mbar_wait_bounded(&q_full, (n_items - 1) & 1, abort_v, kDrainTimeoutNs);
+      }
     }
-  } else if (warp >= 4) {
+  } else if (!PAIR && warp >= 4) {
     // ------------------------------------------------------------ V to fp16
-    // Warp w takes rows 32 w .. 32 w + 31 of each V tile; a lane's 16-byte chunk holds
-    // 8 values of one row.  Rows past the sequence become 0, whatever the page holds. A NaN
-    // becomes 0 too and is noted for its key: the rows that see the key get NaN in
-    // the epilogue, a row that does not is not reached through 0 * NaN.
-    regs_decrease<kRegsConvert>();
-    constexpr int kBlocks = D / 64, kPieces = 8 * kBlocks;  // 16-byte chunks per lane
-    const int w = warp - 4;
+    regs_decrease<C::kRegsConvert>();
     uint32_t g = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Item item;
       ok = next_item(k, item);
       if (!ok || item.s1 == 0) break;
-      for (int s = item.s0; s < item.s1; ++s, ++g) {
-        const uint32_t slot = g % VS;
-        ok = warp_wait(&v_full[slot], (g / VS) & 1, abort_v, kTimeoutNs);
-        if (!ok) break;
-        const int valid = item.kv_len - item.tile(s) * BN;  // rows of the tile that are tokens
-        const uint32_t base = smem_u32(v_s + slot * C::kTileBytes) + w * 32 * 128 + lane * 16;
-        uint4 x[kPieces];
-        uint32_t nans = 0;  // a bit per chunk
-#pragma unroll
-        for (int u = 0; u < kPieces; ++u) x[u] = lds128(base + (u / 8) * C::kColBlockBytes + (u % 8) * 512);
-#pragma unroll
-        for (int u = 0; u < kPieces; ++u) {
-          const int r = 32 * w + 4 * (u % 8) + lane / 8;
-          const bool live = r < valid;
-          x[u].x = live ? bf16x2_to_f16x2(x[u].x) : 0u;
-          x[u].y = live ? bf16x2_to_f16x2(x[u].y) : 0u;
-          x[u].z = live ? bf16x2_to_f16x2(x[u].z) : 0u;
-          x[u].w = live ? bf16x2_to_f16x2(x[u].w) : 0u;
-          if (has_nan_f16x2(x[u].x) || has_nan_f16x2(x[u].y) || has_nan_f16x2(x[u].z) || has_nan_f16x2(x[u].w))
-            nans |= 1u << u;
-        }
-        uint32_t keys = 0;
-        if (__any_sync(0xffffffffu, nans != 0)) {
-#pragma unroll
-          for (int u = 0; u < kPieces; ++u) {
-            uint32_t* y = reinterpret_cast<uint32_t*>(&x[u]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if ((y[i] & 0x7FFFu) > 0x7C00u) y[i] &= 0xFFFF0000u;
-              if (((y[i] >> 16) & 0x7FFFu) > 0x7C00u) y[i] &= 0x0000FFFFu;
-            }
-            const uint32_t hit = __ballot_sync(0xffffffffu, (nans >> u) & 1u);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if ((hit >> (8 * i)) & 0xFFu) keys |= 1u << (4 * (u % 8) + i);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kPieces; ++u) sts128(base + (u / 8) * C::kColBlockBytes + (u % 8) * 512, x[u]);
-        if (lane == 0) nan_keys[g % kReady][w] = keys;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&v_ready[g % kReady]);
-      }
+      for (int s = item.s0; s < item.s1 && ok; ++s, ++g) ok = convert(item, s, g, warp - 4);
     }
     if (!ok && lane == 0) record_abort(abort_v, kSiteConvert);
   } else {
     // ------------------------------------------------------------ softmax, epilogue
-    regs_increase<kRegsSoftmax>();
-    const int r_in = warp * 32 + lane;  // row of the item
-    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-    const uint32_t o_tmem = tmem + lane_off + kTmemO;
+    regs_increase<C::kRegsSoftmax>();
+    const int t = warp / 4;                 // row tile (a pair's second: warps 4 .. 7)
+    const int quarter = warp % 4;           // the warp's TMEM lanes
+    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
     const float c = p.c;
-    uint32_t g = 0;
+    const uint64_t c2 = f2_pack(c, c);
+    uint32_t q = 0, g = 0;                  // products and steps of the launch
+    uint32_t n_joins = 0, n_out = 0;        // joins; items whose O went through this row tile's accumulator
+    // the four softmax warps wait for one another (bounded, as every wait)
+    auto join = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&joined);
+      return warp_wait(&joined, n_joins++ & 1, abort_v, kTimeoutNs);
+    };
+
+    // What a thread keeps of its row of a row tile.
+    struct Row {
+      float m;        // reference value, log2 units
+      float l;        // sum of the fp16-rounded P (normalises O)
+      float l_exact;  // sum of the fp32 P (gives LSE)
+      int lo, hi;     // the row sees keys [lo, hi), the sinks below hi, and the drafted tokens of `words`
+      const uint32_t* words;
+      int flags;  // kLive: a row of the item; kNan: it sees a key whose V holds a NaN; kSeen: every row of
+                  // the warp has seen a key
+    };
+    constexpr int kLive = 1, kNan = 2, kSeen = 4;
+
+    // One item: with NG key groups, group `grp` of 128 / NG lanes holds the rows and takes the keys
+    // [grp * n_cols, (grp + 1) * n_cols) of every tile, 32 at a time.  False when a wait gave up.
+    auto run_item = [&](const Item& item, auto ng) -> bool {
+      constexpr int NG = decltype(ng)::value;
+      constexpr int n_cols = BN / NG, kRows = BM / NG;
+      const int grp = quarter * 32 / kRows;
+      const int row = (quarter * 32) % kRows + lane;  // row of the row tile
+      const int u_tok = token_of(p, row);             // its token within the row tile
+      const int tiles = PAIR && NG == 1 ? item.row_tiles(p.R) : 1;
+      const int n_words = min(p.mask_words, (item.seq_n + 31) / 32);
+      const int sinks = p.window > 0 ? p.sinks : 0;
+      if (t >= tiles) {  // a pair's second warps on an item of one row tile: V alone
+        for (int s = item.s0; s < item.s1; ++s, ++g)
+          if (!convert(item, s, g, warp)) return false;
+        q += item.s1 - item.s0;
+        return true;
+      }
+      auto start = [&]() {
+        Row r;
+        r.m = -INFINITY;
+        r.l = r.l_exact = 0.0f;
+        r.lo = 0;
+        const bool live = row < min(p.R, item.ntok - t * p.R) * p.G;
+        r.flags = live ? kLive : 0;
+        const int tok = t * p.R + u_tok;  // within the item
+        const int u = item.first + tok;   // among the sequence's newest
+        r.words = p.mask && live && item.kv_len > 0 ? p.mask + static_cast<int64_t>(item.tok0 + tok) * p.mask_words
+                                                    : nullptr;
+        r.hi = !live || item.kv_len == 0 ? 0 : p.mask ? item.ctx : item.ctx + u + 1;
+        if (p.window > 0) {
+          int place = item.ctx + u;
+          if (r.words) {
+            place = item.ctx - 1;
+            for (int i = 0; i < n_words; ++i) place += __popc(__ldg(r.words + i) & range_bits(32 * i, 0, item.seq_n));
+          }
+          r.lo = place - p.window + 1;
+        }
+        return r;
+      };
+      Row cur = start();
+      // the keys [key, key + 32) that the row sees
+      auto visible = [&](int key) {
+        uint32_t v = range_bits(key, cur.lo, cur.hi) | range_bits(key, 0, min(sinks, cur.hi));
+        if (cur.words) {
+          const int u0 = key - item.ctx;  // the drafted token of the word's first bit
+          const int at = u0 >> 5;
+          const uint32_t a = at >= 0 && at < n_words ? __ldg(cur.words + at) : 0u;
+          const uint32_t z = at + 1 >= 0 && at + 1 < n_words ? __ldg(cur.words + at + 1) : 0u;
+          v |= __funnelshift_r(a, z, u0 & 31) & range_bits(u0, 0, item.seq_n);
+        }
+        return v;
+      };
+      // tiles that every row of the item sees whole: below `whole_hi` and from `whole_lo` on
+      const int whole_hi = item.kv_len == 0 ? 0 : p.mask ? item.ctx : item.ctx + item.first + 1;
+      const int whole_lo = p.window > 0 ? item.ctx + (p.mask ? item.seq_n : item.first + item.ntok) - p.window : 0;
+      auto is_masked = [&](int s) {
+        const int key = item.tile(s) * BN;
+        return key + BN > whole_hi || (key < whole_lo && key + BN > sinks);
+      };
+      // NaN in the V of keys of step s (step gg of the launch) that the row sees
+      auto look_for_nan = [&](int s, uint32_t gg) {
+        const volatile uint32_t* nk = nan_keys[gg % kReady] + grp * (n_cols / 32);
+        uint32_t any = 0;
+#pragma unroll
+        for (int i = 0; i < n_cols / 32; ++i) any |= nk[i];
+        if (any != 0) {
+          for (int i = 0; i < n_cols / 32; ++i) {
+            const int key = item.tile(s) * BN + grp * n_cols + 32 * i;
+            if (nk[i] & (!(cur.flags & kLive) ? 0u : is_masked(s) ? visible(key) : 0xFFFFFFFFu)) cur.flags |= kNan;
+          }
+        }
+      };
+      const int lag = 3 - tiles;  // steps until a step's PV of the same row tile is known to be complete
+      q += t;
+      for (int s = item.s0; s < item.s1; ++s, ++g, q += tiles) {
+        if (PAIR && !convert(item, s, g, warp)) return false;  // while S is on its way
+        const int key0 = item.tile(s) * BN + grp * n_cols;  // the group's first key of the tile
+        const bool masked = is_masked(s);
+        uint32_t vis_first = 0;
+        if (masked) vis_first = visible(key0);  // before the wait, as its loads may take a while
+        if (!warp_wait(&s_full[q & 1], (q >> 1) & 1, abort_v, kTimeoutNs)) return false;
+        // a warp without rows of the row tile has nothing to do: its lanes are never read
+        if (NG > 1 || __any_sync(0xffffffffu, cur.flags & kLive)) {
+          tc_fence_after();
+          const bool live = cur.flags & kLive;
+          const uint32_t s_tmem = tmem + lane_off + (q & 1) * BN + grp * n_cols;
+          const uint32_t p_tmem = tmem + lane_off + (C::kOverS ? (q & 1) * BN : kTmemP + (q & 1) * (BN / 2));
+          // 32 columns of S, -inf where the row does not see the key
+          auto load_s = [&](int col, uint32_t (&r)[32]) {
+            tmem_ld32_wait(s_tmem + col, r);
+            if (masked) {
+              const uint32_t w = col == 0 ? vis_first : visible(key0 + col);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = (w >> e) & 1u ? r[e] : __float_as_uint(-INFINITY);
+            }
+          };
+          auto max_of = [&](const uint32_t (&r)[32]) {
+            float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              x = max3f(x, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+              y = max3f(y, __uint_as_float(r[e + 2]), __uint_as_float(r[e + 3]));
+            }
+            return fmaxf(x, y);
+          };
+          float alpha = 1.0f;  // what the row's sums and O are scaled by
+          if (!(cur.flags & kSeen)) {  // m: 6 below the max of the row's first keys
+            float top = -INFINITY;
+#pragma unroll 1
+            for (int col = 0; col < n_cols; col += 32) {
+              uint32_t r[32];
+              load_s(col, r);
+              top = fmaxf(top, max_of(r));
+            }
+            if (live && cur.m == -INFINITY && top > -INFINITY) {
+              cur.m = top * c - kStart;
+              alpha = 0.0f;
+            }
+            if (!__any_sync(0xffffffffu, live && cur.m == -INFINITY)) cur.flags |= kSeen;
+          }
+          // P against m into TMEM, 32 keys at a time, and its sums
+          float sum = 0.0f, sum_exact = 0.0f;
+#pragma unroll 1
+          for (int col = 0; col < n_cols; col += 32) {
+            uint32_t r[32], pk[16];
+            load_s(col, r);
+            float part, part_exact;
+            auto exponentials = [&]() {
+              const float neg_m = cur.m == -INFINITY ? 0.0f : -cur.m;
+              const uint64_t nm2 = f2_pack(neg_m, neg_m);
+              uint64_t e0 = f2_pack(0.0f, 0.0f), e1 = e0;
+              float q0 = 0.0f, q1 = 0.0f, q2 = 0.0f, q3 = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                float x0, x1;
+                f2_unpack(ffma2(f2_pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c2, nm2), x0, x1);
+                const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+                pk[e] = pack_f16x2(p0, p1);
+                if (e & 1) {
+                  e1 = fadd2(e1, f2_pack(p0, p1));
+                  add_f16x2_to_f32(q2, q3, pk[e]);
+                } else {
+                  e0 = fadd2(e0, f2_pack(p0, p1));
+                  add_f16x2_to_f32(q0, q1, pk[e]);
+                }
+              }
+              float a0, a1, b0, b1;
+              f2_unpack(e0, a0, a1);
+              f2_unpack(e1, b0, b1);
+              part_exact = (a0 + a1) + (b0 + b1);
+              part = (q0 + q1) + (q2 + q3);
+            };
+            exponentials();
+            // Rare: P may have passed fp16's largest value (a NaN fails the comparison too).  m moves to 6
+            // below these keys' max; what the tile has of P and of its sums is scaled like O.
+            const bool over = live && !(part_exact <= kF16Max);
+            if (__any_sync(0xffffffffu, over)) {
+              const float m_new = max_of(r) * c - kStart;
+              float a = 1.0f;
+              if (over && m_new > cur.m) {
+                a = ex2_approx(cur.m - m_new);
+                cur.m = m_new;
+              }
+              alpha *= a;
+              sum *= a;
+              sum_exact *= a;
+              for (int done = 0; done < col; done += 32) {
+                const uint32_t at = p_tmem + (grp * n_cols + done) / 2;
+                tmem_wait_st();
+                tmem_ld16_wait(at, pk);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) pk[e] = mul_f16x2(pk[e], a);
+                tmem_st16(at, pk);
+              }
+              exponentials();
+            }
+            sum += part;
+            sum_exact += part_exact;
+            tmem_st16(p_tmem + (grp * n_cols + col) / 2, pk);
+          }
+          if (__any_sync(0xffffffffu, alpha != 1.0f)) {
+            cur.l *= alpha;
+            cur.l_exact *= alpha;
+            if (s > item.s0) {
+              // O is scaled once PV of the last step is complete.  With two row tiles that is q - 2, and
+              // S(q) came after it.  With one it is q - 1, and PV(q) waits for this warp, so that the
+              // barrier is in phase q - 1 or has just left it.
+              if (tiles == 1 && !warp_wait(&pv_done, (q - 1) & 1, abort_v, kTimeoutNs)) return false;
+              tc_fence_after();
+              const uint64_t a2 = f2_pack(alpha, alpha);
+#pragma unroll 1
+              for (int cb = 0; cb < D / 32; ++cb) {
+                const uint32_t at = tmem + lane_off + kTmemO + t * D + cb * 32;
+                uint32_t o[32];
+                tmem_ld32_wait(at, o);
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                  float x0, x1;
+                  f2_unpack(fmul2(f2_pack(__uint_as_float(o[e]), __uint_as_float(o[e + 1])), a2), x0, x1);
+                  o[e] = __float_as_uint(x0);
+                  o[e + 1] = __float_as_uint(x1);
+                }
+                tmem_st32(at, o);
+              }
+            }
+          }
+          cur.l += sum;
+          cur.l_exact += sum_exact;
+          if (NG > 1 && (C::kOverS || s - item.s0 < 2)) {
+            // P of the other groups' keys: 0.  Columns of their own keep it for the whole item.
+            uint32_t zero[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) zero[e] = 0u;
+            for (int e = 0; e < BN / 2; e += 16)
+              if (e / (n_cols / 2) != grp) tmem_st16(p_tmem + e, zero);
+          }
+          tmem_wait_st();
+          tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[q & 1]);
+        // the V tiles of products before S(q) had been converted
+        if (s - item.s0 >= lag) look_for_nan(s - lag, g - lag);
+      }
+      q -= t;
+      // ---- epilogue, when the row tile's last PV is complete
+      const bool whole = item.out == 0;
+      {
+        if (!warp_wait(&o_full[t], n_out++ & 1, abort_v, kTimeoutNs)) return false;
+        tc_fence_after();
+        for (int s = max(item.s1 - lag, item.s0); s < item.s1; ++s) look_for_nan(s, g - (item.s1 - s));
+        const bool live = cur.flags & kLive;
+        const int rows = min(p.R, item.ntok - t * p.R) * p.G;
+        const uint32_t o_tmem = tmem + lane_off + kTmemO + t * D;
+        if (cur.flags & kNan) cur.l = __int_as_float(0x7FC00000);
+        // where a row's result goes: element `at` x D of o, or of the partials
+        auto place = [&](int r) {
+          const int u = token_of(p, r);
+          return whole ? static_cast<int64_t>(item.tok0 + t * p.R + u) * p.Hq + item.h * p.G + r - u * p.G
+                       : static_cast<int64_t>(2 * blockIdx.x + item.out - 1) * (2 * BM) + t * BM + r;
+        };
+        auto put_lse = [&](float lse2) {
+          if (whole)
+            p.lse[place(row)] = lse2 * 0.69314718055994531f;
+          else
+            p.part_lse[place(row)] = lse2;
+        };
+        if (NG == 1) {
+          // l is NaN when S or P was; a row without keys has l == 0, and its O is 0 (P was)
+          const float inv = cur.l == 0.0f ? 0.0f : 1.0f / cur.l;
+          const int64_t at = place(row);
+          if (__any_sync(0xffffffffu, live)) {
+#pragma unroll 1
+            for (int cb = 0; cb < D / 32; ++cb) {
+              uint32_t o[32];
+              tmem_ld32_wait(o_tmem + 32 * cb, o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
+              if (live && whole) {
+                uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + 32 * cb);
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                  uint32_t w[4];
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)
+                    w[e] = pack_bf16x2(__uint_as_float(o[8 * ch + 2 * e]), __uint_as_float(o[8 * ch + 2 * e + 1]));
+                  dst[ch] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+              } else if (live) {
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + 32 * cb);
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch)
+                  dst[ch] = make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
+              }
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&o_empty[t]);  // the next item's first PV may overwrite O
+          if (live) put_lse(cur.l == 0.0f ? -INFINITY : cur.m + lg2_approx(cur.l_exact));
+        } else {
+          // The groups' sums of a row, each against its own m, are joined in the last V slot, which the
+          // issuer left to the epilogue: m and the sums in its last 2 KB, O below them, in two halves
+          // of the columns if there is not room for all.
+          uint8_t* stage = v_s + ((g - 1) % VS) * C::kTileBytes;
+          float4* stat = reinterpret_cast<float4*>(stage + C::kTileBytes - BM * 16);
+          stat[grp * kRows + row] = make_float4(cur.m, cur.l, cur.l_exact, 0.0f);
+          if (!join()) return false;
+          float m_all = -INFINITY, l_all = 0.0f, x_all = 0.0f;
+#pragma unroll
+          for (int i = 0; i < NG; ++i) m_all = fmaxf(m_all, stat[i * kRows + row].x);
+          const float ref = m_all == -INFINITY ? 0.0f : m_all;
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            const float4 st = stat[i * kRows + row];
+            const float f = ex2_approx(st.x - ref);
+            l_all += f * st.y;
+            x_all += f * st.z;
+          }
+          const float mul = l_all == 0.0f ? 0.0f : ex2_approx(cur.m - ref) / l_all;
+          if (live && grp == 0) put_lse(l_all == 0.0f ? -INFINITY : ref + lg2_approx(x_all));
+          const int passes = NG * rows * D * 4 <= C::kTileBytes - BM * 16 ? 1 : 2;
+          const int width = D / passes, quads = width / 4;  // columns, and 16-byte pieces of a row, per pass
+          const int quad_bits = 31 - __clz(quads);
+          float4* piece = reinterpret_cast<float4*>(stage);
+          if (passes > 1 && !join()) return false;  // m and the sums have been read
+#pragma unroll 1
+          for (int col = 0; col < D; col += width) {
+            if (col > 0 && !join()) return false;  // the stage has been read
+#pragma unroll 1
+            for (int cb = 0; cb < width / 32; ++cb) {
+              uint32_t o[32];
+              tmem_ld32_wait(o_tmem + col + 32 * cb, o);
+              if (live) {
+#pragma unroll
+                for (int ch = 0; ch < 8; ++ch) {
+                  float4 x;
+                  x.x = __uint_as_float(o[4 * ch]) * mul;
+                  x.y = __uint_as_float(o[4 * ch + 1]) * mul;
+                  x.z = __uint_as_float(o[4 * ch + 2]) * mul;
+                  x.w = __uint_as_float(o[4 * ch + 3]) * mul;
+                  // pieces of a row swizzled by the row: lanes write and read without bank conflicts
+                  const int to = 8 * cb + ch;
+                  piece[(grp * rows + row) * quads + (to ^ (row & 7))] = x;
+                }
+              }
+            }
+            if (col + width == D) {
+              tc_fence_before();
+              mbar_arrive(&o_empty[t]);  // the next item's first PV may overwrite O
+            }
+            if (!join()) return false;
+            for (int e = quarter * 32 + lane; e < rows * quads; e += 128) {
+              const int rr = e >> quad_bits, from = e & (quads - 1);
+              float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+              for (int i = 0; i < NG; ++i) {
+                const float4 y = piece[(i * rows + rr) * quads + (from ^ (rr & 7))];
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+              }
+              const int64_t to = place(rr) * D + col + 4 * from;
+              if (whole)
+                *reinterpret_cast<uint2*>(p.o + to) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+              else
+                *reinterpret_cast<float4*>(p.part_o + to) = x;
+            }
+          }
+          fence_proxy_async_smem();  // the slot is the TMA's again
+          if (!join()) return false;
+          if (threadIdx.x == 0) mbar_arrive(&v_empty[(g - 1) % VS]);
+        }
+      }
+      return true;
+    };
+
     bool ok = true;
     for (int k = 0; ok; ++k) {
       Item item;
       ok = next_item(k, item);
       if (!ok || item.s1 == 0) break;
-      const int rows = item.ntok * p.G;
-      const bool live = r_in < rows;
-      const bool warp_live = warp * 32 < rows;
-      const int u_tok = r_in / p.G;       // token of the row within the item
-      const int u = item.first + u_tok;   // ... among the sequence's newest tokens
-      const uint32_t* words = (p.mask && live) ? p.mask + static_cast<int64_t>(item.tok0 + u_tok) * p.mask_words : nullptr;
-      const int n_words = min(p.mask_words, (item.seq_n + 31) / 32);
-      // the row's limits: keys [lo, hi) and the sinks below hi; drafted tokens by the mask
-      const int hi = !live || item.kv_len == 0 ? 0 : p.mask ? item.ctx : item.ctx + u + 1;
-      int lo = 0;
-      if (p.window > 0) {
-        int place = item.ctx + u;
-        if (words) {
-          place = item.ctx - 1;
-          for (int i = 0; i < n_words; ++i) place += __popc(__ldg(words + i) & range_bits(32 * i, 0, item.seq_n));
-        }
-        lo = place - p.window + 1;
-      }
-      const int sinks = p.window > 0 ? p.sinks : 0;
-      // tiles that every row of the item sees whole: below `whole_hi` and from `whole_lo` on
-      const int whole_hi = item.kv_len == 0 ? 0 : p.mask ? item.ctx : item.ctx + item.first + 1;
-      const int whole_lo = p.window > 0 ? item.ctx + (p.mask ? item.seq_n : item.first + item.ntok) - p.window : 0;
-      float m = -INFINITY;   // reference value, log2 units
-      float l = 0.0f;        // sum of the fp16-rounded P (normalises O)
-      float l_exact = 0.0f;  // sum of the fp32 P (gives LSE)
-      bool nan_row = false;
-      for (int s = item.s0; s < item.s1; ++s, ++g) {
-        const int key0 = item.tile(s) * BN;
-        const bool masked = key0 + BN > whole_hi || (key0 < whole_lo && key0 + BN > sinks);
-        uint32_t vis[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = key0 + 32 * i;
-            vis[i] = range_bits(key, lo, hi) | range_bits(key, 0, min(sinks, hi));
-            if (words) {
-              const int u0 = key - item.ctx;  // the drafted token of the word's first bit
-              const int at = u0 >> 5;
-              const uint32_t a = at >= 0 && at < n_words ? __ldg(words + at) : 0u;
-              const uint32_t z = at + 1 >= 0 && at + 1 < n_words ? __ldg(words + at + 1) : 0u;
-              if (item.kv_len > 0) vis[i] |= __funnelshift_r(a, z, u0 & 31) & range_bits(u0, 0, item.seq_n);
-            }
-          }
-        } else if (!live) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vis[i] = 0u;
-        }
-        ok = warp_wait(&s_full[g & 1], (g >> 1) & 1, abort_v, kTimeoutNs);
-        if (!ok) break;
-        if (!warp_live) {  // no row: nothing of these lanes is ever read
-          mbar_arrive(&p_full[g & 1]);
-          continue;
-        }
-        tc_fence_after();
-        const uint32_t s_tmem = tmem + lane_off + (g & 1) * BN;
-        uint32_t r[128];
-        tmem_ld128_wait(s_tmem, r);
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 128; ++i) r[i] = (vis[i / 32] >> (i % 32)) & 1u ? r[i] : __float_as_uint(-INFINITY);
-        }
-        float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 128; i += 8) {
-          mx0 = max3f(mx0, __uint_as_float(r[i + 0]), __uint_as_float(r[i + 1]));
-          mx1 = max3f(mx1, __uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
-          mx2 = max3f(mx2, __uint_as_float(r[i + 4]), __uint_as_float(r[i + 5]));
-          mx3 = max3f(mx3, __uint_as_float(r[i + 6]), __uint_as_float(r[i + 7]));
-        }
-        const float top = live ? fmaxf(max3f(mx0, mx1, mx2), mx3) * c : -INFINITY;
-        // m moves when the row sees its first key, or P would pass 2^15
-        float alpha = 1.0f;
-        if (top > m + kLimit || (m == -INFINITY && top > -INFINITY)) {
-          const float m_new = top - kStart;
-          alpha = ex2_approx(m - m_new);  // 0 from -inf
-          m = m_new;
-          l *= alpha;
-          l_exact *= alpha;
-        }
-        if (s > item.s0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-          // PV(g-1) has to be complete.  PV(g-2) is, as S(g) was issued after it, and PV(g) waits for
-          // this warp, so the barrier is in phase g-1 or has just left it
-          ok = warp_wait(&pv_done, (g - 1) & 1, abort_v, kTimeoutNs);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a2 = f2_pack(alpha, alpha);
-#pragma unroll
-          for (int cb = 0; cb < D / 32; ++cb) {
-            uint32_t o[32];
-            tmem_ld32_wait(o_tmem + cb * 32, o);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float x0, x1;
-              f2_unpack(fmul2(f2_pack(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), a2), x0, x1);
-              o[i] = __float_as_uint(x0);
-              o[i + 1] = __float_as_uint(x1);
-            }
-            tmem_st32(o_tmem + cb * 32, o);
-          }
-        }
-        const float neg_m = m == -INFINITY ? 0.0f : -m;
-        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(neg_m, neg_m);
-        uint64_t e0 = f2_pack(0.0f, 0.0f), e1 = e0;
-        float q0 = 0.0f, q1 = 0.0f, q2 = 0.0f, q3 = 0.0f;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t pk[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int e = 64 * half + 2 * i;
-            float x0, x1;
-            f2_unpack(ffma2(f2_pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), c2, nm2), x0, x1);
-            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-            pk[i] = pack_f16x2(p0, p1);
-            if (i & 1) {
-              e1 = fadd2(e1, f2_pack(p0, p1));
-              add_f16x2_to_f32(q2, q3, pk[i]);
-            } else {
-              e0 = fadd2(e0, f2_pack(p0, p1));
-              add_f16x2_to_f32(q0, q1, pk[i]);
-            }
-          }
-          tmem_st32(s_tmem + 64 + 32 * half, pk);
-        }
-        tmem_wait_st();
-        tc_fence_before();
-        mbar_arrive(&p_full[g & 1]);
-        float a0, a1, b0, b1;
-        f2_unpack(e0, a0, a1);
-        f2_unpack(e1, b0, b1);
-        l_exact += (a0 + a1) + (b0 + b1);
-        l += (q0 + q1) + (q2 + q3);
-        // NaN among the V that the row sees
-        ok = warp_wait(&v_ready[g % kReady], (g / kReady) & 1, abort_v, kTimeoutNs);
-        if (!ok) break;
-        const uint4 nk = lds128(smem_u32(nan_keys[g % kReady]));
-        nan_row |= ((nk.x & vis[0]) | (nk.y & vis[1]) | (nk.z & vis[2]) | (nk.w & vis[3])) != 0;
-      }
-      if (!ok) break;
-      // ---- epilogue, when the item's last PV is complete
-      ok = warp_wait(&o_full, k & 1, abort_v, kTimeoutNs);
-      if (!ok) break;
-      tc_fence_after();
-      // l is NaN when S or P was; a row without keys has l == 0
-      const bool none = l == 0.0f && !nan_row;
-      const float inv = none ? 0.0f : nan_row ? __int_as_float(0x7FC00000) : 1.0f / l;
-      const float lse2 = none ? -INFINITY : m + lg2_approx(l_exact);
-      const bool whole = item.out == 0;
-      const int64_t at = whole ? static_cast<int64_t>(item.tok0 + u_tok) * p.Hq + item.h * p.G + r_in % p.G
-                               : static_cast<int64_t>(2 * blockIdx.x + item.out - 1) * BM + r_in;
-      if (warp_live) {
-        // 32 columns at a time; O of a row without keys is whatever the MMA made of P = 0, and not used
-#pragma unroll
-        for (int cb = 0; cb < D / 32; ++cb) {
-          uint32_t o[32];
-          tmem_ld32_wait(o_tmem + 32 * cb, o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = none ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-          if (live && whole) {
-            uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + 32 * cb);
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16x2(__uint_as_float(o[8 * ch + 2 * i]), __uint_as_float(o[8 * ch + 2 * i + 1]));
-              dst[ch] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else if (live) {
-            uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + 32 * cb);
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-              dst[ch] = make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
-          }
-        }
-        if (live) {
-          if (whole)
-            p.lse[at] = lse2 * 0.69314718055994531f;
-          else
-            p.part_lse[at] = lse2;
-        }
-      }
-      tc_fence_before();
-      mbar_arrive(&o_empty);  // the next item's first PV may overwrite O
+      const int groups = item.groups(p.G);
+      if (groups == 4)
+        ok = run_item(item, std::integral_constant<int, 4>{});
+      else if (groups == 2)
+        ok = run_item(item, std::integral_constant<int, 2>{});
+      else
+        ok = run_item(item, std::integral_constant<int, 1>{});
     }
     if (!ok && lane == 0) record_abort(abort_v, kSiteSoftmax);
   }
@@ -824,12 +1197,13 @@ template <int D>
 __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const Params p) {
   constexpr int kVec = D / 32;
   griddep_wait();
-  const int4 d = p.desc[blockIdx.x];
+  const int4 d = p.desc[blockIdx.x];  // tokens, first token, kv head, last CTA
   const int lane = threadIdx.x % 32;
-  const int row = blockIdx.y * 8 + threadIdx.x / 32;
-  if (row >= d.x) return;
+  const int row = blockIdx.y * 8 + threadIdx.x / 32;  // of the two row tiles that an item may have
+  const int t = row / BM, u = token_of(p, row % BM);
+  if (row % BM >= min(p.R, d.x - t * p.R) * p.G) return;
   const int n = d.w - static_cast<int>(blockIdx.x) + 1;  // ranges: slot 1 of this CTA, slot 0 of the next ones
-  auto slot = [&](int i) { return static_cast<int64_t>(2 * (blockIdx.x + i) + (i == 0)) * BM + row; };
+  auto slot = [&](int i) { return static_cast<int64_t>(2 * (blockIdx.x + i) + (i == 0)) * (2 * BM) + row; };
   float top = -INFINITY;
   for (int i = lane; i < n; i += 32) top = fmaxf(top, p.part_lse[slot(i)]);
 #pragma unroll
@@ -849,7 +1223,7 @@ __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const Params p) {
     }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const int64_t at = static_cast<int64_t>(d.y + row / p.G) * p.Hq + d.z * p.G + row % p.G;
+  const int64_t at = static_cast<int64_t>(d.y + t * p.R + u) * p.Hq + d.z * p.G + row % BM - u * p.G;
 #pragma unroll
   for (int v = 0; v < kVec; v += 2)
     *reinterpret_cast<uint32_t*>(p.o + at * D + lane * kVec + v) = pack_bf16x2(acc[v] * inv, acc[v + 1] * inv);
@@ -874,11 +1248,16 @@ int prepare_device(int dev) {
   if (dev < 0 || dev >= kMax) return ATTN_ERR_UNSUPPORTED_DEVICE;
   std::lock_guard<std::mutex> lock(mutex);
   if (ready[dev]) return ATTN_OK;
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn_tree_kernel<128>),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::kSmemBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(attn_tree_kernel<64>),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<64>::kSmemBytes);
+  const struct {
+    const void* kernel;
+    int bytes;
+  } all[] = {{reinterpret_cast<const void*>(attn_tree_kernel<128, false>), Cfg<128, false>::kSmemBytes},
+             {reinterpret_cast<const void*>(attn_tree_kernel<128, true>), Cfg<128, true>::kSmemBytes},
+             {reinterpret_cast<const void*>(attn_tree_kernel<64, false>), Cfg<64, false>::kSmemBytes},
+             {reinterpret_cast<const void*>(attn_tree_kernel<64, true>), Cfg<64, true>::kSmemBytes}};
+  cudaError_t e = cudaSuccess;
+  for (const auto& x : all)
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(x.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, x.bytes);
   if (e != cudaSuccess) return cuda_fail(e);
   if (!attn_host::encode_tiled_fn()) return ATTN_ERR_TENSOR_MAP;
   ready[dev] = true;
@@ -906,6 +1285,32 @@ bool encode_pages(CUtensorMap* map, const attn_kv_cache& c, const void* base, in
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_queries(QMaps* maps, const void* q, int64_t token, int64_t head, int n_tokens, int Hkv, int G, int D) {
+  attn_host::EncodeTiledFn fn = attn_host::encode_tiled_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(G), static_cast<cuuint64_t>(Hkv),
+                              static_cast<cuuint64_t>(n_tokens)};
+  // the stride of a dimension of one element is not used, but has to be valid
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(G > 1 ? head * 2 : D * 2),
+                                 static_cast<cuuint64_t>(Hkv > 1 ? head * G * 2 : D * 2),
+                                 static_cast<cuuint64_t>(n_tokens > 1 ? token * 2 : D * 2)};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  CUtensorMap* all[3] = {&maps->rows128, &maps->rows64, &maps->rows32};
+  for (int i = 0; i < 3; ++i) {
+    // with more heads than a box of 64 or 32 rows holds no item has that many groups
+    const cuuint32_t tokens = static_cast<cuuint32_t>(std::max((BM >> i) / G, 1));
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, tokens};
+    if (i > 0 && (BM >> i) < G) {
+      *all[i] = *all[0];
+    } else if (fn(all[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, step,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS) {
+      return false;
+    }
+  }
+  return true;
+}
+
 struct Workspace {
   size_t o, lse, desc, bytes;  // offsets, and in all
 };
@@ -913,8 +1318,8 @@ struct Workspace {
 Workspace layout(int D) {
   Workspace w;
   w.o = 0;
-  w.lse = w.o + sizeof(float) * kMaxCtas * 2 * BM * D;
-  w.desc = w.lse + sizeof(float) * kMaxCtas * 2 * BM;
+  w.lse = w.o + sizeof(float) * kMaxCtas * 2 * 2 * BM * D;
+  w.desc = w.lse + sizeof(float) * kMaxCtas * 2 * 2 * BM;
   w.bytes = w.desc + sizeof(int4) * kMaxCtas;
   return w;
 }
@@ -926,16 +1331,21 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
 }
 
 template <int D>
-int launch(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int sms, cudaStream_t stream) {
+int launch(const QMaps& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int sms, cudaStream_t stream) {
   const int grid = std::min(sms, kMaxCtas);
-  attn_tree_kernel<D><<<grid, kThreads, Cfg<D>::kSmemBytes, stream>>>(tk, tv, p);
+  if (p.item_tokens > p.R)
+    attn_tree_kernel<D, true><<<grid, kThreads, Cfg<D, true>::kSmemBytes, stream>>>(tq, tk, tv, p);
+  else
+    attn_tree_kernel<D, false><<<grid, kThreads, Cfg<D, false>::kSmemBytes, stream>>>(tq, tk, tv, p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, (std::min(p.R, p.n_tokens) * p.G + 7) / 8);
+  // rows of an item: one row tile's, or all of the first's places and the second's
+  const int rows = p.n_tokens <= p.R ? p.n_tokens * p.G : p.item_tokens == p.R ? p.R * p.G : BM + p.R * p.G;
+  cfg.gridDim = dim3(grid, (rows + 7) / 8);
   cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -961,7 +1371,8 @@ int attn_fwd_tree(const attn_kv_cache* cache, const void* q, int64_t q_stride_to
   if (n_tokens < 0 || Hq < 1 || Hq % c.Hkv != 0 || Hq / c.Hkv > BM) return ATTN_ERR_INVALID_ARG;
   if (window < 0 || sinks < 0 || !(std::isfinite(scale) && scale > 0.0f)) return ATTN_ERR_INVALID_ARG;
   if (tree_mask ? mask_words < 1 : mask_words != 0) return ATTN_ERR_INVALID_ARG;
-  if (q_stride_token < 0 || q_stride_head < 0 || q_stride_token % 8 != 0 || q_stride_head % 8 != 0)
+  if ((Hq > 1 && (q_stride_head < c.D || q_stride_head % 8 != 0 || q_stride_head > (INT64_MAX / 8) / Hq)) ||
+      (n_tokens > 1 && (q_stride_token < c.D || q_stride_token % 8 != 0 || q_stride_token > (INT64_MAX / 8) / n_tokens)))
     return ATTN_ERR_INVALID_ARG;
   if (n_tokens == 0 || c.rows == 0) return ATTN_OK;
   if (!q || !o || !lse || !cu_tokens || !workspace) return ATTN_ERR_NULL_PTR;
@@ -980,7 +1391,8 @@ int attn_fwd_tree(const attn_kv_cache* cache, const void* q, int64_t q_stride_to
     const void* at;
     size_t bytes;
   } outs[] = {{o, static_cast<size_t>(heads) * c.D * 2}, {lse, static_cast<size_t>(heads) * 4}, {workspace, w.bytes}},
-    ins[] = {{q, static_cast<size_t>((n_tokens - 1) * q_stride_token + (Hq - 1) * q_stride_head + c.D) * 2},
+    ins[] = {{q, static_cast<size_t>((n_tokens > 1 ? (n_tokens - 1) * q_stride_token : 0) +
+                                    (Hq > 1 ? (Hq - 1) * q_stride_head : 0) + c.D) * 2},
              {c.n_pages > 0 ? c.k : nullptr, static_cast<size_t>(std::max<int64_t>(kv_end[0], 0)) * 2},
              {c.n_pages > 0 ? c.v : nullptr, static_cast<size_t>(std::max<int64_t>(kv_end[1], 0)) * 2},
              {c.page_table, static_cast<size_t>(c.rows) * c.max_pages * 4},
@@ -1002,15 +1414,14 @@ int attn_fwd_tree(const attn_kv_cache* cache, const void* q, int64_t q_stride_to
   if (sms == 0) return ATTN_ERR_UNSUPPORTED_DEVICE;
   st = prepare_device(dev);
   if (st != ATTN_OK) return st;
+  QMaps tq;
   CUtensorMap tk, tv;
-  if (!encode_pages(&tk, c, c.k, c.k_stride_page, c.k_stride_head, c.k_stride_slot, q) ||
+  if (!encode_queries(&tq, q, q_stride_token, q_stride_head, n_tokens, c.Hkv, Hq / c.Hkv, c.D) ||
+      !encode_pages(&tk, c, c.k, c.k_stride_page, c.k_stride_head, c.k_stride_slot, q) ||
       !encode_pages(&tv, c, c.v, c.v_stride_page, c.v_stride_head, c.v_stride_slot, q))
     return ATTN_ERR_TENSOR_MAP;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Params p;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.q_token = q_stride_token;
-  p.q_head = q_stride_head;
   p.o = static_cast<__nv_bfloat16*>(o);
   p.lse = lse;
   p.cu = cu_tokens;
@@ -1027,13 +1438,18 @@ int attn_fwd_tree(const attn_kv_cache* cache, const void* q, int64_t q_stride_to
   p.Hkv = c.Hkv;
   p.G = Hq / c.Hkv;
   p.R = BM / p.G;
+  // Pairs of row tiles, which share each key tile, when the sequences have more tokens than a row tile
+  // on average (130 us instead of 152, see the head).  With fewer the second softmax warps would only
+  // convert, and V has a slot less: one token each, 272 us instead of 240 (D 128), 135 instead of 109 (D 64).
+  p.item_tokens = n_tokens > static_cast<int64_t>(p.R) * c.rows ? 2 * p.R : p.R;
+  p.G_inv = (65536u + p.G - 1) / p.G;
   p.window = std::min(window, 1 << 30);  // no key is further away (rows hold less than 2^31 tokens)
   p.sinks = std::min(sinks, 1 << 30);
   p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.part_o = reinterpret_cast<float*>(ws + w.o);
   p.part_lse = reinterpret_cast<float*>(ws + w.lse);
   p.desc = reinterpret_cast<int4*>(ws + w.desc);
-  return c.D == 128 ? launch<128>(tk, tv, p, sms, stream) : launch<64>(tk, tv, p, sms, stream);
+  return c.D == 128 ? launch<128>(tq, tk, tv, p, sms, stream) : launch<64>(tq, tk, tv, p, sms, stream);
 }
 
 const char* attn_paged_strerror(int status) { return attn_host::status_text(status, t_last_cuda_error); }

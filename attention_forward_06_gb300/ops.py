@@ -7,10 +7,11 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
-from ._lib import KvCache, load
+from ._lib import load
 
 ATTN_OK = 0
 ATTN_ERR_INVALID_ARG = 1
@@ -35,8 +36,8 @@ def _check(status: int) -> None:
 
 
 def _stream_handle(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: a Stream object costs 3 us of a call's host time
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -238,34 +239,45 @@ def attn_fwd_ordered(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tile_ord
     return o, lse
 
 
-def _on_device(**tensors) -> torch.device:
-    """The one CUDA device that all of the given tensors (None: absent) lie on, which has to be the current one."""
-    dev = None
+def _on_device(**tensors) -> int:
+    """The index of the one CUDA device that all of the given tensors (None: absent) lie on, which has to be the
+    current one."""
+    index = -1
+    for t in tensors.values():
+        if t is not None:
+            i = t.get_device()
+            if index < 0:
+                index = i
+            if i < 0 or i != index:
+                break
+    else:
+        if index == torch.cuda.current_device():
+            return index
     for name, t in tensors.items():
-        if t is None:
-            continue
-        if not t.is_cuda:
+        if t is not None and not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the tensors before it on {dev}")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {dev}, the current device is {torch.cuda.current_device()}")
-    return dev
+    raise ValueError("the tensors have to be on the current device: " +
+                     ", ".join(f"{name} is on {t.device}" for name, t in tensors.items() if t is not None))
+
+
+def _is(t: torch.Tensor, dtype: torch.dtype, shape) -> bool:
+    """A contiguous tensor of this type and shape?"""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
 
 
 def _window_shapes(q, k, v, window, sinks, causal):
     for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or not t.is_contiguous() or t.dim() != 4:
+        if t.dtype is not torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous 4-d bf16 CUDA tensor")
-    if v.shape != k.shape or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3]:
+    B, Hq, Sq, D = q.shape
+    Bk, Hkv, Sk, Dk = k.shape
+    if v.shape != k.shape or Bk != B or Dk != D:
         raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
     if causal not in (1, 2):
         raise ValueError("causal must be 1 (bottom-right) or 2 (top-left)")
     if window < 1 or sinks < 0:
         raise ValueError("window must be at least 1 and sinks at least 0")
-    return (*q.shape[:2], k.shape[1], q.shape[2], k.shape[2], q.shape[3])
+    return B, Hq, Hkv, Sq, Sk, D
 
 
 _INT_MAX = 2 ** 31 - 1
@@ -280,16 +292,16 @@ def attn_fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: i
     ``p_i`` is ``i + Sk - Sq`` (causal 1) or ``i`` (causal 2).  A row without keys gets ``o = 0``, ``lse = -inf``.
     """
     B, Hq, Hkv, Sq, Sk, D = _window_shapes(q, k, v, window, sinks, causal)
-    _on_device(q=q, k=k, v=v, o=o, lse=lse)
+    device = _on_device(q=q, k=k, v=v, o=o, lse=lse)
     if scale is None:
         scale = 1.0 / math.sqrt(D)
     if o is None:
         o = torch.empty_like(q)
-    elif o.shape != q.shape or o.dtype != torch.bfloat16 or not o.is_contiguous():
+    elif not _is(o, torch.bfloat16, q.shape):
         raise ValueError("o must be a contiguous bf16 tensor shaped like q")
     if lse is None:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=q.device)
-    elif tuple(lse.shape) != (B, Hq, Sq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=device)
+    elif not _is(lse, torch.float32, (B, Hq, Sq)):
         raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, Sq]")
     _check(load().attn_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
                                   Sq, Sk, D, int(causal), min(int(window), _INT_MAX), min(int(sinks), _INT_MAX),
@@ -352,11 +364,11 @@ def attn_bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
     when not given.
     """
     B, Hq, Hkv, Sq, Sk, D = _window_shapes(q, k, v, window, sinks, causal)
-    _on_device(q=q, k=k, v=v, o=o, lse=lse, dout=dout, dq=dq, dk=dk, dv=dv, workspace=workspace)
+    device = _on_device(q=q, k=k, v=v, o=o, lse=lse, dout=dout, dq=dq, dk=dk, dv=dv, workspace=workspace)
     for name, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
-        if t is not None and (t.dtype != torch.bfloat16 or t.shape != like.shape or not t.is_contiguous()):
+        if t is not None and not _is(t, torch.bfloat16, like.shape):
             raise ValueError(f"{name} must be a contiguous bf16 tensor of shape {tuple(like.shape)}")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, Sq) or not lse.is_contiguous():
+    if not _is(lse, torch.float32, (B, Hq, Sq)):
         raise ValueError("lse must be the forward's contiguous fp32 [B, Hq, Sq]")
     if workspace is not None and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
@@ -367,7 +379,7 @@ def attn_bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
     dv = torch.empty_like(v) if dv is None else dv
     if workspace is None:
         need = bwd_window_workspace_size(B, Hq, Hkv, Sq, Sk, D, window, sinks)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
     lib = load("attn_bwd")
     st = lib.attn_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
                              dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Sk, D, int(causal),
@@ -382,29 +394,43 @@ def attn_bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
 KV_INVALID = -1  # device status: lengths, indices or lists that do not fit each other (ATTN_KV_INVALID)
 
 
-def _int32(name: str, t: torch.Tensor, *shape) -> torch.Tensor:
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or \
-            any(n is not None and t.shape[i] != n for i, n in enumerate(shape)):
-        want = ", ".join("n" if n is None else str(n) for n in shape)
-        raise ValueError(f"{name} must be a contiguous int32 tensor [{want}]")
+def _int32(name: str, t: torch.Tensor, n: int | None = None) -> torch.Tensor:
+    """``t``, which has to be a contiguous int32 vector (of n entries)."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be a contiguous int32 tensor [{'n' if n is None else n}]")
     return t
 
 
-def _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts=None) -> KvCache:
-    """The C ABI's cache of ``k_pages``/``v_pages [pages, Hkv, page_size, D]`` (any strides but the last, 1)."""
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if t.dtype != torch.bfloat16 or t.dim() != 4 or t.stride(3) != 1:
-            raise ValueError(f"{name} must be a 4-d bf16 tensor [pages, Hkv, page_size, D] whose last stride is 1")
-    if v_pages.shape != k_pages.shape:
-        raise ValueError(f"shape mismatch k_pages{tuple(k_pages.shape)} v_pages{tuple(v_pages.shape)}")
-    n_pages, Hkv, page_size, D = k_pages.shape
-    rows, max_pages = _int32("page_table", page_table, None, None).shape
+_pack_cache = struct.Struct("2P6q3P6i").pack  # attn_kv_cache (include/attn_kv.h)
+
+
+def _page_table(page_table, seq_lens) -> tuple[int, int]:
+    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
+        raise ValueError("page_table must be a contiguous int32 tensor [rows, max_pages]")
+    rows, max_pages = page_table.shape
     _int32("seq_lens", seq_lens, rows)
-    if ref_counts is not None:
-        _int32("ref_counts", ref_counts, n_pages)
-    return KvCache(k_pages.data_ptr(), v_pages.data_ptr(), *k_pages.stride()[:3], *v_pages.stride()[:3],
-                   page_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr() if ref_counts is not None else None,
-                   n_pages, Hkv, page_size, D, rows, max_pages)
+    return rows, max_pages
+
+
+def _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts=None):
+    """The C ABI's cache of ``k_pages``/``v_pages [pages, Hkv, page_size, D]`` (any strides but the last, 1), and
+    ``rows, Hkv, D``."""
+    shape, (kp, kh, ks, k1), (vp, vh, vs, v1) = k_pages.shape, _strides(k_pages), _strides(v_pages)
+    if k_pages.dtype is not torch.bfloat16 or v_pages.dtype is not torch.bfloat16 or k1 != 1 or v1 != 1:
+        raise ValueError("k_pages and v_pages must be bf16 tensors [pages, Hkv, page_size, D] whose last stride is 1")
+    if v_pages.shape != shape:
+        raise ValueError(f"shape mismatch k_pages{tuple(shape)} v_pages{tuple(v_pages.shape)}")
+    n_pages, Hkv, page_size, D = shape
+    rows, max_pages = _page_table(page_table, seq_lens)
+    refs = _int32("ref_counts", ref_counts, n_pages).data_ptr() if ref_counts is not None else 0
+    return _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), kp, kh, ks, vp, vh, vs, page_table.data_ptr(),
+                       seq_lens.data_ptr(), refs, n_pages, Hkv, page_size, D, rows, max_pages), rows, Hkv, D
+
+
+def _strides(pages) -> tuple:
+    if pages.dim() != 4:
+        raise ValueError("k_pages and v_pages must be 4-d tensors [pages, Hkv, page_size, D]")
+    return pages.stride()
 
 
 def _check_kv(status: int) -> None:
@@ -412,7 +438,7 @@ def _check_kv(status: int) -> None:
         raise AttnError(status, load("attn_kv").attn_kv_strerror(status).decode())
 
 
-def _status(status, n: int, device) -> torch.Tensor:
+def _status(status, n: int, device: int) -> torch.Tensor:
     return torch.empty(n, dtype=torch.int32, device=device) if status is None else _int32("status", status, n)
 
 
@@ -427,16 +453,15 @@ def kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor, v
     """
     dev = _on_device(k_pages=k_pages, v_pages=v_pages, k_new=k_new, v_new=v_new, page_table=page_table,
                      seq_lens=seq_lens, ref_counts=ref_counts, cu_tokens=cu_tokens, status=status)
-    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
+    cache, rows, Hkv, D = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
+    n = k_new.shape[0]
     for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape[1:] != (cache.Hkv, cache.D) or t.stride(2) != 1:
-            raise ValueError(f"{name} must be a bf16 tensor [tokens, {cache.Hkv}, {cache.D}] whose last stride is 1")
-    if v_new.shape != k_new.shape:
-        raise ValueError(f"shape mismatch k_new{tuple(k_new.shape)} v_new{tuple(v_new.shape)}")
-    _int32("cu_tokens", cu_tokens, cache.rows + 1)
+        if t.dtype is not torch.bfloat16 or t.shape != (n, Hkv, D) or t.stride(2) != 1:
+            raise ValueError(f"{name} must be a bf16 tensor [{n}, {Hkv}, {D}] whose last stride is 1")
+    _int32("cu_tokens", cu_tokens, rows + 1)
     status = _status(status, 1, dev)
     _check_kv(load("attn_kv").attn_kv_append(cache, k_new.data_ptr(), v_new.data_ptr(), *k_new.stride()[:2],
-                                             *v_new.stride()[:2], k_new.shape[0], cu_tokens.data_ptr(),
+                                             *v_new.stride()[:2], n, cu_tokens.data_ptr(),
                                              status.data_ptr(), _stream_handle(stream)))
     return status
 
@@ -450,8 +475,8 @@ def kv_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tens
     """
     dev = _on_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
                      ref_counts=ref_counts, parents=parents, children=children, status=status)
-    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
-    n = _int32("parents", parents, None).shape[0]
+    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)[0]
+    n = _int32("parents", parents).shape[0]
     _int32("children", children, n)
     status = _status(status, 1, dev)
     _check_kv(load("attn_kv").attn_kv_fork(cache, parents.data_ptr(), children.data_ptr(), n, status.data_ptr(),
@@ -471,11 +496,11 @@ def kv_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.T
     dev = _on_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
                      ref_counts=ref_counts, cu_tokens=cu_tokens, accepted=accepted, cu_accepted=cu_accepted,
                      status=status)
-    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
-    _int32("cu_tokens", cu_tokens, cache.rows + 1)
-    _int32("cu_accepted", cu_accepted, cache.rows + 1)
-    _int32("accepted", accepted, None)
-    status = _status(status, cache.rows, dev)
+    cache, rows, _, _ = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
+    _int32("cu_tokens", cu_tokens, rows + 1)
+    _int32("cu_accepted", cu_accepted, rows + 1)
+    _int32("accepted", accepted)
+    status = _status(status, rows, dev)
     _check_kv(load("attn_kv").attn_kv_compact(cache, cu_tokens.data_ptr(), accepted.data_ptr(), accepted.shape[0],
                                               cu_accepted.data_ptr(), status.data_ptr(), _stream_handle(stream)))
     return status
@@ -488,12 +513,11 @@ def kv_free(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.
     A row listed twice is freed once; one that is out of range is passed over.
     """
     _on_device(page_table=page_table, seq_lens=seq_lens, ref_counts=ref_counts, rows=rows)
-    n_rows, max_pages = _int32("page_table", page_table, None, None).shape
-    _int32("seq_lens", seq_lens, n_rows)
-    n_pages = _int32("ref_counts", ref_counts, None).shape[0]
-    n = _int32("rows", rows, None).shape[0]
-    cache = KvCache(page_table=page_table.data_ptr(), seq_lens=seq_lens.data_ptr(), ref_counts=ref_counts.data_ptr(),
-                    n_pages=n_pages, Hkv=1, page_size=int(page_size), D=64, rows=n_rows, max_pages=max_pages)
+    n_rows, max_pages = _page_table(page_table, seq_lens)
+    n_pages = _int32("ref_counts", ref_counts).shape[0]
+    n = _int32("rows", rows).shape[0]
+    cache = _pack_cache(0, 0, 0, 0, 0, 0, 0, 0, page_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
+                        n_pages, 1, int(page_size), 64, n_rows, max_pages)  # heads and D are not used
     _check_kv(load("attn_kv").attn_kv_free(cache, rows.data_ptr(), n, _stream_handle(stream)))
 
 
@@ -528,11 +552,14 @@ def attn_fwd_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     """
     dev = _on_device(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
                      cu_tokens=cu_tokens, tree_mask=tree_mask, o=o, lse=lse, workspace=workspace)
-    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens)
-    if q.dtype != torch.bfloat16 or q.dim() != 3 or q.stride(2) != 1 or q.shape[2] != cache.D:
-        raise ValueError(f"q must be a bf16 tensor [tokens, Hq, {cache.D}] whose last stride is 1")
-    T, Hq, D = q.shape
-    _int32("cu_tokens", cu_tokens, cache.rows + 1)
+    cache, rows, _, D = _kv_cache(k_pages, v_pages, page_table, seq_lens)
+    if q.dtype is not torch.bfloat16 or q.dim() != 3:
+        raise ValueError(f"q must be a bf16 tensor [tokens, Hq, {D}] whose last stride is 1")
+    T, Hq, Dq = q.shape
+    q_token, q_head, q_last = q.stride()
+    if Dq != D or q_last != 1:
+        raise ValueError(f"q must be a bf16 tensor [tokens, Hq, {D}] whose last stride is 1")
+    _int32("cu_tokens", cu_tokens, rows + 1)
     words = 0
     if tree_mask is not None:
         if tree_mask.element_size() != 4 or tree_mask.dim() != 2 or tree_mask.shape[0] != T or \
@@ -541,11 +568,11 @@ def attn_fwd_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
         words = tree_mask.shape[1]
     if o is None:
         o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    elif tuple(o.shape) != (T, Hq, D) or o.dtype != torch.bfloat16 or not o.is_contiguous():
+    elif not _is(o, torch.bfloat16, (T, Hq, D)):
         raise ValueError("o must be a contiguous bf16 tensor shaped like q")
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    elif tuple(lse.shape) != (T, Hq) or lse.dtype != torch.float32 or not lse.is_contiguous():
+    elif not _is(lse, torch.float32, (T, Hq)):
         raise ValueError("lse must be a contiguous fp32 tensor [tokens, Hq]")
     lib = load("attn_paged")
     if workspace is None:
@@ -554,7 +581,7 @@ def attn_fwd_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
         raise ValueError("workspace must be contiguous")
     if scale is None:
         scale = 1.0 / math.sqrt(D)
-    st = lib.attn_fwd_tree(cache, q.data_ptr(), q.stride(0), q.stride(1), o.data_ptr(), lse.data_ptr(), T, Hq,
+    st = lib.attn_fwd_tree(cache, q.data_ptr(), q_token, q_head, o.data_ptr(), lse.data_ptr(), T, Hq,
                            cu_tokens.data_ptr(), tree_mask.data_ptr() if tree_mask is not None else None, words,
                            min(int(window), _INT_MAX), min(int(sinks), _INT_MAX), float(scale), workspace.data_ptr(),
                            workspace.numel() * workspace.element_size(), _stream_handle(stream))

@@ -22,7 +22,7 @@
  * cu_tokens[0] and from cu_tokens[rows] on belong to no row: o and lse keep what they hold there.
  *
  * Layout.  q: bf16, element (token, head, d) at token * q_stride_token + head *
- * q_stride_head + d (multiples of 8).  o: bf16 [n_tokens][Hq][D], lse: fp32
+ * q_stride_head + d (multiples of 8, at least D).  o: bf16 [n_tokens][Hq][D], lse: fp32
  * [n_tokens][Hq], contiguous.  cu_tokens int32 [rows + 1], tree_mask uint32
  * [n_tokens][mask_words] or NULL.  D is 64 or 128; Hq a multiple of Hkv, at most 128 query
  * heads per kv head; scale finite and positive; q, o, lse and the workspace 16-byte

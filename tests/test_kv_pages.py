@@ -294,7 +294,7 @@ def fake(**kw):
     a = dict(k=0x1000000, v=0x2000000, k_stride_page=2 * 16 * 64, k_stride_head=16 * 64, k_stride_slot=64,
              v_stride_page=2 * 16 * 64, v_stride_head=16 * 64, v_stride_slot=64, page_table=0x3000000,
              seq_lens=0x3100000, ref_counts=0x3200000, n_pages=10, Hkv=2, page_size=16, D=64, rows=4, max_pages=5)
-    return _lib.KvCache(**dict(a, **kw))
+    return ctypes.byref(_lib.KvCache(**dict(a, **kw)))
 
 
 def call_append(lib, cache, k=0x4000000, n=4, cu=0x5000000, status=0x5100000, stride=128):

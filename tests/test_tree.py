@@ -7,6 +7,7 @@ Tolerances are the dense entry points' (parity_util): |dO| <= 1e-2 below 4 and |
 fp32 and its weight 2^x by an instruction of relative error below 2^-21, so cutting a sequence into ranges adds nothing
 that shows beside the rounding of O to bf16.
 """
+import ctypes
 import os
 import re
 
@@ -376,8 +377,8 @@ def test_exports_what_the_header_declares(lib):
 
 def test_workspace_size(lib):
     for D in (64, 128):
-        # 192 CTAs: two partials of 128 rows (D values and an LSE each), and 16 bytes
-        assert ops.tree_workspace_size(D) == 192 * (2 * 128 * (D + 1) * 4 + 16)
+        # 160 CTAs: two partials of 256 rows (D values and an LSE each), and 16 bytes
+        assert ops.tree_workspace_size(D) == 160 * (2 * 256 * (D + 1) * 4 + 16)
     assert lib.attn_fwd_tree_workspace_size(96) == 0
 
 
@@ -386,7 +387,7 @@ def fake(**kw):
     a = dict(k=0x1000000, v=0x2000000, k_stride_page=2 * 16 * 64, k_stride_head=16 * 64, k_stride_slot=64,
              v_stride_page=2 * 16 * 64, v_stride_head=16 * 64, v_stride_slot=64, page_table=0x3000000,
              seq_lens=0x3100000, ref_counts=None, n_pages=10, Hkv=2, page_size=16, D=64, rows=4, max_pages=5)
-    return _lib.KvCache(**dict(a, **kw))
+    return ctypes.byref(_lib.KvCache(**dict(a, **kw)))
 
 
 def call(lib, cache=None, **kw):
@@ -398,7 +399,7 @@ def call(lib, cache=None, **kw):
 
 @pytest.mark.parametrize("kw", [dict(Hq=7), dict(Hq=0), dict(Hq=258), dict(T=-1), dict(window=-1), dict(sinks=-1),
                                 dict(scale=0.0), dict(scale=float("inf")), dict(words=0), dict(mask=None),
-                                dict(q_token=4), dict(q_head=-64), dict(n=1000), dict(o=0x4000000), dict(lse=0x5000000),
+                                dict(q_token=4), dict(q_head=-64), dict(q_head=0), dict(n=1000), dict(o=0x4000000), dict(lse=0x5000000),
                                 dict(ws=0x1000000), dict(ws=0x4000000), dict(o=0x3000000 - 64), dict(o=0x7100000)],
                          ids=lambda k: "-".join(map(str, k.items())))
 def test_arguments_that_are_refused(lib, kw):
