@@ -97,6 +97,7 @@ constexpr uint64_t kTimeoutNs = 4000000000ull;  // 4 s per wait
 constexpr uint64_t kDrainTimeoutNs = 500000000ull;
 constexpr float kHeadroom = 8.0f;       // log2 units: m is set this far above a tile's row max
 constexpr int kHeadroomBits = 8;
+constexpr int kFewKeys = 16;            // window mode: keys of a step for a few sinks (one K step of the MMA)
 constexpr float kF16Max = 65504.0f;     // largest finite fp16: a tile's P mass above it may overflow
 constexpr float kScaleMassLimit = 18446744073709551616.0f;  // 2^64: beyond it a tile is redone from S
 
@@ -155,6 +156,7 @@ struct Params {
   // window mode: key j also needs row + diag - j < window or j < sinks
   int window;  // 1 .. max(Sq, Sk)
   int sinks;   // 0 .. Sk
+  int pairs;   // 1: an item's Q tiles are the same 128 rows of two heads of a group, 0: 256 rows of a head
 };
 
 struct Item {
@@ -164,7 +166,9 @@ struct Item {
   int j0;       // first key tile
   int n_tiles;  // key tiles to visit
   int split;    // key range index (split-key mode)
+  int row_step, head_step;  // Q tile t: rows from q0 + t * row_step, head bh + t * head_step
   int n_sink;   // window mode: the first n_sink tiles visited are key tiles 0 .. n_sink - 1, the rest start at j0
+  bool few;     // ... the first is visited for its first kFewKeys keys alone, which hold all sinks
 };
 
 // Item x of the heaviest-first list: query block from the last, then (split-key
@@ -194,13 +198,25 @@ __device__ __forceinline__ Item item_at(const Params& p, int x) {
     it.bh = x % p.BH;
     it.split = 0;
   }
+  it.row_step = BM;
+  it.head_step = 0;
+  int rows = ROWS_PER_ITEM;
+  if constexpr (WINDOW) {
+    if (p.pairs) {
+      qb = p.n_qtiles - 1 - x / (p.BH / 2);
+      it.bh = 2 * (x % (p.BH / 2));
+      it.row_step = 0;
+      it.head_step = 1;
+      rows = BM;
+    }
+  }
   const int b = it.bh / p.Hq;
   const int hq = it.bh % p.Hq;
   it.kv_z = b * p.Hkv + hq / p.G;
-  it.q0 = qb * ROWS_PER_ITEM;
+  it.q0 = qb * rows;
   int kv_end = p.Sk;
   if (p.causal) {
-    const int last_row = min(it.q0 + ROWS_PER_ITEM, p.Sq) - 1;
+    const int last_row = min(it.q0 + rows, p.Sq) - 1;
     kv_end = min(p.Sk, last_row + p.diag + 1);
   }
   const int n_full = kv_end > 0 ? (kv_end + BN - 1) / BN : 0;
@@ -213,6 +229,8 @@ __device__ __forceinline__ Item item_at(const Params& p, int x) {
     it.j0 = min(max(it.q0 + p.diag - p.window + 1, 0) / BN, n_full);
     it.n_sink = min((max(min(p.sinks, kv_end), 0) + BN - 1) / BN, it.j0);
     it.n_tiles = it.n_sink + n_full - it.j0;
+    // (32 / 8 heads, 32768 tokens, window 1024, 4 sinks, D 128: 497 us, 516 with the whole tile)
+    it.few = it.n_sink == 1 && p.sinks <= kFewKeys;
   } else {
     it.j0 = 0;
     it.n_tiles = n_full;  // block-sparse mode: the causal bound; the producer counts the marked tiles
@@ -554,8 +572,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < QTILES; ++t)
 #pragma unroll
         for (int cb = 0; cb < D / 64; ++cb)
-          tma_load_3d_elect(q_s + t * C::kTileBytes + cb * C::kColBlockBytes, &tq, &q_full, cb * 64, it.q0 + t * BM,
-                            it.bh);
+          tma_load_3d_elect(q_s + t * C::kTileBytes + cb * C::kColBlockBytes, &tq, &q_full, cb * 64,
+                            it.q0 + t * it.row_step, it.bh + t * it.head_step);
       ++q_issued;
       // block-sparse mode: the marked key tiles in order (find-first-set over the union words)
       MaskRows mrows{};
@@ -627,23 +645,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Operand descriptors are built once per tile; a K step moves the start
     // address field (bits 0-13, address >> 4) by a constant, never carrying out.
     // each issue ends with commits to up to two mbarriers (kNoBar: none)
-    auto issue_s = [=](int t, uint32_t slot, uint32_t bar0 = kNoBar, uint32_t bar1 = kNoBar) {
+    uint32_t idesc_s1 = idesc_s;  // of an item's first step (window mode: of kFewKeys keys perhaps)
+    bool few = false;
+    auto issue_s = [=](int t, uint32_t slot, uint32_t bar0 = kNoBar, uint32_t bar1 = kNoBar, uint32_t idesc = 0u) {
       const uint64_t qd = sdesc_sw128(opaque(q_addr) + t * C::kTileBytes, 16, 1024);
       const uint64_t kd = sdesc_sw128(kv_addr + slot * C::kTileBytes, 16, 1024);
       static_assert(C::kColBlockBytes == 16384, "K-step offsets of mma_bf16_ss_k8");
       if constexpr (D == 128)
-        mma_bf16_ss_k8(tmem + t * BN, qd, kd, idesc_s, bar0, bar1);
+        mma_bf16_ss_k8(tmem + t * BN, qd, kd, WINDOW && idesc ? idesc : idesc_s, bar0, bar1);
       else
-        mma_bf16_ss_k4(tmem + t * BN, qd, kd, idesc_s, bar0, bar1);
+        mma_bf16_ss_k4(tmem + t * BN, qd, kd, WINDOW && idesc ? idesc : idesc_s, bar0, bar1);
     };
     const uint32_t ones_addr = smem_u32(ones_s);
-    auto issue_pv = [=](int t, uint32_t slot, bool accumulate, uint32_t bar0 = kNoBar, uint32_t bar1 = kNoBar) {
+    auto issue_pv = [=, &few](int t, uint32_t slot, bool accumulate, uint32_t bar0 = kNoBar, uint32_t bar1 = kNoBar) {
       // V is MN-major: the leading byte offset steps from one 64-column block of V to
       // the next; at D = 64 the second block is the ones block (the row-sum columns)
       const uint32_t v_addr = opaque(kv_addr) + slot * C::kTileBytes;
       const uint64_t vd =
           sdesc_sw128(v_addr, C::kTensorRowSum ? ones_addr - v_addr : C::kColBlockBytes, 1024);
       static_assert(BN == 128, "K steps of mma_bf16_ts_k8");
+      if constexpr (WINDOW) {
+        if (few && !accumulate) {  // the item's first step: its first kFewKeys keys
+          static_assert(kFewKeys == 16, "one K step");
+          mma_bf16_ts_k1(tmem + 2 * BN + t * 128, tmem + t * BN + 64, vd, idesc_pv, 0u, bar0, bar1);
+          return;
+        }
+      }
       mma_bf16_ts_k8(tmem + 2 * BN + t * 128, tmem + t * BN + 64, vd, idesc_pv, accumulate ? 1u : 0u, bar0, bar1);
     };
     // wait for load number `n` of the K/V stream (a K tile), or for its conversion (a V tile)
@@ -662,7 +689,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       int x, n_marked = 0;
       ok = next_item(k, x, LISTED ? &n_marked : nullptr);
       if (!ok || x < 0) break;
-      const int n = LISTED ? n_marked : item_at<SPLIT, false, GROUPED, WINDOW>(p, x).n_tiles;
+      int n;
+      if constexpr (WINDOW) {
+        const Item it = item_at<SPLIT, false, GROUPED, WINDOW>(p, x);
+        n = it.n_tiles;
+        few = it.few;
+        idesc_s1 = few ? idesc_bf16_f32(BM, kFewKeys, false) : idesc_s;
+      } else {
+        n = LISTED ? n_marked : item_at<SPLIT, false, GROUPED, WINDOW>(p, x).n_tiles;
+      }
       if (n == 0) continue;
       ok = warp_wait(&q_full, n_done & 1, abort_v, kTimeoutNs);
       if (ok) ok = wait_kv(kv_it);
@@ -671,8 +706,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++kv_it;
       tc_fence_after();
       ATTN_TR(12, x);  // item start: its first S products
-      issue_s(0, kslot, smem_u32(&s_full[0]));
-      issue_s(1, kslot, smem_u32(&s_full[1]), smem_u32(&kv_empty[kslot]));
+      issue_s(0, kslot, smem_u32(&s_full[0]), kNoBar, idesc_s1);
+      issue_s(1, kslot, smem_u32(&s_full[1]), smem_u32(&kv_empty[kslot]), idesc_s1);
       if (n == 1) mma_commit_elect(&q_empty);
       // One step: P.V of both Q tiles on V_j and, unless it is the item's last, their S on K_(j+1).
       // At D = 64, where the softmax sets the pace, the first, second-last and last steps are separate
@@ -795,7 +830,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint8_t* stage = st_s + ((C::kStageBufs == 1) ? 0 : t) * C::kStageBytes;
 #pragma unroll
           for (int cb = 0; cb < D / 64; ++cb)
-            tma_store_3d_elect(&to, stage + cb * (BM * 128), cb * 64, it.q0 + t * BM, it.bh);
+            tma_store_3d_elect(&to, stage + cb * (BM * 128), cb * 64, it.q0 + t * it.row_step,
+                               it.bh + t * it.head_step);
           bulk_commit_group_elect();
           ATTN_TR(30, t);  // O stores of Q tile t issued
           bulk_wait_group_read0();  // the staging tile has been read: hand it on
@@ -833,12 +869,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (x < 0) break;
       const Item it = item_at<SPLIT, SPARSE, GROUPED, WINDOW>(p, x);
       const int n_tiles = LISTED ? n_marked : it.n_tiles;  // key tiles the item visits
-      const int row = it.q0 + t * BM + quarter * 32 + lane;  // global query row
+      const int row = it.q0 + t * it.row_step + quarter * 32 + lane;  // global query row
+      const int bh = it.bh + t * it.head_step;
       const bool live = row < p.Sq;
-      __nv_bfloat16* orow = p.o + (static_cast<int64_t>(it.bh) * p.Sq + row) * D;
-      float* lrow = p.lse + static_cast<int64_t>(it.bh) * p.Sq + row;
+      __nv_bfloat16* orow = p.o + (static_cast<int64_t>(bh) * p.Sq + row) * D;
+      float* lrow = p.lse + static_cast<int64_t>(bh) * p.Sq + row;
       // split-key mode: this item's partial result rows
-      const int64_t prow = (static_cast<int64_t>(it.split) * p.BH + it.bh) * p.Sq + row;
+      const int64_t prow = (static_cast<int64_t>(it.split) * p.BH + bh) * p.Sq + row;
       if (n_tiles == 0) {  // no key is visible to any row of this item (or its key range is empty)
         if (live) {
           if (SPLIT) {
@@ -856,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // last allowed key of this row, and of the tile's first row (the most restricted)
-      const int tile_row0 = it.q0 + t * BM;
+      const int tile_row0 = it.q0 + t * it.row_step;
       int lim = p.Sk - 1, lim_tile = p.Sk - 1;
       if (p.causal) {
         lim = min(lim, row + p.diag);
@@ -918,18 +955,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vn = 2u * g + 1u;
           ok = warp_wait(&kv_full[vn % S], (vn / S) & 1, abort_v, kTimeoutNs);
           if (!ok) break;
-          constexpr int kChunks = C::kTileBytes / 16 / 256;  // per thread: 8 (D = 128) or 4 (D = 64)
-          const uint32_t base = smem_u32(kv_s + (vn % S) * C::kTileBytes) + 16u * threadIdx.x;
-          uint4 w[kChunks];
+          if (WINDOW && it.few && j == 0) {  // the first kFewKeys rows of each column block: 128 chunks
+            const uint32_t at = smem_u32(kv_s + (vn % S) * C::kTileBytes) + 16u * (threadIdx.x % 128) +
+                                (threadIdx.x / 128) * C::kColBlockBytes;
+            if (static_cast<int>(threadIdx.x) < 128 * (D / 64)) {
+              uint4 w = lds128(at);
+              w.x = bf16x2_to_f16x2(w.x);
+              w.y = bf16x2_to_f16x2(w.y);
+              w.z = bf16x2_to_f16x2(w.z);
+              w.w = bf16x2_to_f16x2(w.w);
+              sts128(at, w);
+            }
+          } else {
+            constexpr int kChunks = C::kTileBytes / 16 / 256;  // per thread: 8 (D = 128) or 4 (D = 64)
+            const uint32_t base = smem_u32(kv_s + (vn % S) * C::kTileBytes) + 16u * threadIdx.x;
+            uint4 w[kChunks];
 #pragma unroll
-          for (int u = 0; u < kChunks; ++u) w[u] = lds128(base + 4096u * u);
+            for (int u = 0; u < kChunks; ++u) w[u] = lds128(base + 4096u * u);
 #pragma unroll
-          for (int u = 0; u < kChunks; ++u) {
-            w[u].x = bf16x2_to_f16x2(w[u].x);
-            w[u].y = bf16x2_to_f16x2(w[u].y);
-            w[u].z = bf16x2_to_f16x2(w[u].z);
-            w[u].w = bf16x2_to_f16x2(w[u].w);
-            sts128(base + 4096u * u, w[u]);
+            for (int u = 0; u < kChunks; ++u) {
+              w[u].x = bf16x2_to_f16x2(w[u].x);
+              w[u].y = bf16x2_to_f16x2(w[u].y);
+              w[u].z = bf16x2_to_f16x2(w[u].z);
+              w[u].w = bf16x2_to_f16x2(w[u].w);
+              sts128(base + 4096u * u, w[u]);
+            }
           }
           fence_proxy_async_smem();  // this thread's writes are visible to the tensor cores' reads
           __syncwarp();
@@ -950,6 +1000,44 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) z[i] = 0u;
             tmem_st32(s_tmem + 64, z);
             tmem_st32(s_tmem + 96, z);
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&p_full[t]);
+            ATTN_TR(21, j);
+            continue;
+          }
+        }
+        if constexpr (WINDOW) {
+          if (it.few && j == 0) {
+            // The sinks alone: kFewKeys columns of S, and P over the first columns of its place (the
+            // product reads no others).  m is set from their max, so P is at most 2^-8.
+            uint32_t f[32];
+            tmem_ld32_wait(s_tmem, f);
+            const int n_vis = min(p.sinks, kmax + 1);
+            float mx = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kFewKeys; ++i) {
+              f[i] = i < n_vis ? f[i] : __float_as_uint(-INFINITY);
+              mx = fmaxf(mx, __uint_as_float(f[i]));
+            }
+            mx *= c;
+            if (mx > m) m = mx + kHeadroom;
+            const float neg_m = (m == -INFINITY) ? 0.0f : -m;
+            float q0 = 0.0f, q1 = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (i < kFewKeys / 2) {
+                const float p0 = ex2_approx(fmaf(__uint_as_float(f[2 * i]), c, neg_m));
+                const float p1 = ex2_approx(fmaf(__uint_as_float(f[2 * i + 1]), c, neg_m));
+                l_exact += p0 + p1;
+                f[i] = pack_f16x2(p0, p1);
+                add_f16x2_to_f32(q0, q1, f[i]);
+              } else {
+                f[i] = 0u;
+              }
+            }
+            if constexpr (!C::kTensorRowSum) l += q0 + q1;
+            tmem_st32(s_tmem + 64, f);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&p_full[t]);
@@ -1460,6 +1548,7 @@ int prepare_launch(const void* q, const void* k, const void* v, void* o, float* 
   prm.mask_words = 0;
   prm.window = 1;
   prm.sinks = 0;
+  prm.pairs = 0;
   prm.n_qtiles = static_cast<int>((Sq + BM - 1) / BM);
   // persistent: one CTA per SM (shared memory and TMEM allow no second), never more CTAs than items
   L->grid = static_cast<int>(items < g_dev_sms[L->dev] ? items : g_dev_sms[L->dev]);
@@ -1700,6 +1789,16 @@ int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float*
   if (st != ATTN_OK || L.empty) return st;
   L.prm.window = std::min(window, std::max(std::max(Sq, Sk), 1));  // no visible key is further away
   L.prm.sinks = std::min(sinks, Sk);
+  // Two heads of a group that need the same keys: 128 rows see a window one tile shorter than 256 do
+  // (window 1024: 9
+  // tiles and the sinks' instead of 10; 32 / 8 heads, 32768 tokens, D 128: 514 us instead of 552).
+  if (Hq / Hkv % 2 == 0) {
+    L.prm.pairs = 1;
+    const int64_t items = static_cast<int64_t>(L.prm.BH) / 2 * L.prm.n_qtiles;
+    if (items > INT32_MAX) return ATTN_ERR_INVALID_ARG;
+    L.prm.n_items = static_cast<int>(items);
+    L.grid = static_cast<int>(std::min<int64_t>(items, g_dev_sms[L.dev]));
+  }
   return D == 128 ? launch<128, false, false, false, false, true>(L, stream)
                   : launch<64, false, false, false, false, true>(L, stream);
 }

@@ -343,6 +343,18 @@ __device__ __forceinline__ void mma_bf16_ts_k4(uint32_t d_tmem, uint32_t a_tmem,
       ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(bar0), "r"(bar1)
       : "memory");
 }
+// TS form over one K step of 16.
+__device__ __forceinline__ void mma_bf16_ts_k1(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                               uint32_t accumulate, uint32_t bar0 = kNoBar, uint32_t bar1 = kNoBar) {
+  asm volatile(
+      "{\n\t.reg .pred e, f, c;\n\t"
+      "setp.ne.b32 f, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, f;\n\t"
+      ATTN_COMMITS(5, 6) "}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(bar0), "r"(bar1)
+      : "memory");
+}
 #undef ATTN_MMA_TS_STEP
 #undef ATTN_COMMITS
 

@@ -33,6 +33,9 @@ CASES = [
     (1, 2, 2, 200, 900, 64, 2, 33, 1),         # keys no row sees
     (1, 2, 1, 2500, 2500, 128, 1, 5, 3),       # the sinks' tile in three chunks
     (1, 4, 1, 2500, 2600, 64, 1, 200, 260),    # three tiles with sinks, each in chunks
+    (1, 4, 2, 900, 900, 128, 1, 100, 16),      # as many sinks as a step of few keys holds, and one more
+    (1, 4, 2, 900, 900, 64, 1, 100, 17),
+    (1, 3, 1, 900, 900, 64, 1, 300, 16),       # three heads of a group: 256 rows of each
     (1, 2, 1, 300, 300, 128, 1, 10 ** 9, 0),   # the window holds everything
     (1, 2, 1, 300, 300, 64, 1, 20, 10 ** 9),   # every key is a sink
     (1, 1, 1, 1, 1, 64, 2, 1, 0),
