@@ -6,6 +6,7 @@ Loading fails loudly when a library is missing: there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 
@@ -13,6 +14,7 @@ from . import build as _build
 
 _lock = threading.Lock()
 _libs: dict[str, ctypes.CDLL] = {}
+_binding = None
 
 _c_int, _c_float, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_void_p
 
@@ -111,3 +113,22 @@ def load(name: str = "attn_fwd", build_if_missing: bool = False) -> ctypes.CDLL:
             f.argtypes = args
         _libs[name] = lib
         return lib
+
+
+def binding():
+    """The extension module that takes torch tensors to the window, paged and cache entry points (csrc/binding.cpp)."""
+    global _binding
+    if _binding is None:
+        with _lock:
+            path = _build.binding_path()
+            if not os.path.exists(path):
+                raise LibraryMissing(
+                    f"{path} is missing: build it with `python -m attention_forward_06_gb300.build` "
+                    "(the CUDA path has no fallback)")
+            import torch  # noqa: F401  (its libraries have to be loaded first)
+
+            spec = importlib.util.spec_from_file_location("attn_binding", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            _binding = module
+    return _binding

@@ -8,6 +8,8 @@
     libattn_paged.so      attention over such a cache (include/attn_paged.h)
     libattn_probe.so      primitive checks of their building blocks (include/attn_fwd_probe.h)
 
+    attn_binding.so       torch tensors to the window, paged and cache entry points (csrc/binding.cpp)
+
 The translation units compile in parallel; a library is rebuilt only when a
 source or header is newer than it.  Usage: ``python -m attention_forward_06_gb300.build``.
 """
@@ -18,6 +20,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -80,17 +83,56 @@ def _compile(name: str, src: str, extra: list[str]) -> tuple[str, str]:
     return out, log
 
 
+def binding_path() -> str:
+    return os.path.join(BUILD_DIR, "attn_binding.so")
+
+
+def _run(cmd: list[str], what: str) -> None:
+    proc = subprocess.run(cmd, capture_output=True, text=True)
+    if proc.returncode != 0:
+        raise RuntimeError(f"g++ failed for {what}:\n{proc.stdout}{proc.stderr}")
+
+
+def _compile_binding() -> str:
+    """binding.cpp to an object file (with this interpreter's torch); linked once the libraries it calls are there."""
+    import torch
+
+    inc = [os.path.join(os.path.dirname(torch.__file__), "include"), sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    obj = binding_path() + f".tmp{os.getpid()}.o"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj, "-I", INCLUDE]
+         + [f"-isystem{i}" for i in inc], "binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = binding_path() + f".tmp{os.getpid()}"
+    _run(["g++", "-shared", obj, "-o", tmp, f"-L{BUILD_DIR}"]
+         + [f"-l:lib{n}.so" for n in ("attn_fwd", "attn_bwd", "attn_kv", "attn_paged")]
+         + [f"-L{lib}", "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python",
+            "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "attn_binding.so")
+    os.remove(obj)
+    os.replace(tmp, binding_path())
+
+
 def build(force: bool = False, verbose: bool = False) -> dict[str, str]:
     """Compile every stale library; return {name: path}."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     todo = {n: s for n, s in LIBS.items() if force or _stale(n)}
-    if todo:
-        with ThreadPoolExecutor(max_workers=len(todo)) as ex:
+    bind = force or bool(todo) or not os.path.exists(binding_path())
+    if todo or bind:
+        with ThreadPoolExecutor(max_workers=len(todo) + 1) as ex:
+            obj = ex.submit(_compile_binding) if bind else None
             futs = {n: ex.submit(_compile, n, src, extra) for n, (src, extra) in todo.items()}
             for n, f in futs.items():
                 _, log = f.result()
                 if verbose:
                     sys.stdout.write(log)
+            if obj is not None:
+                _link_binding(obj.result())
     return {n: lib_path(n) for n in LIBS}
 
 

@@ -1053,9 +1053,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if constexpr (WINDOW) {
           if (masked_low) {
-            const int k0 = max(ksink, 0);  // keys k0 .. kmin - 1 of the tile are masked
+            if (ksink <= 0) {
 #pragma unroll
-            for (int i = 0; i < 128; ++i) r[i] = (i < kmin && i >= k0) ? __float_as_uint(-INFINITY) : r[i];
+              for (int i = 0; i < 128; ++i) r[i] = i < kmin ? __float_as_uint(-INFINITY) : r[i];
+            } else {  // the tile's first ksink keys are sinks
+#pragma unroll
+              for (int i = 0; i < 128; ++i) r[i] = (i < kmin && i >= ksink) ? __float_as_uint(-INFINITY) : r[i];
+            }
           }
         }
         const float m_in = m;  // the reference value the tile starts from

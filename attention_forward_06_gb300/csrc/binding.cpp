@@ -1,0 +1,330 @@
+// binding.cpp -- Python's way to the window, paged and cache-page entry points: it
+// checks torch tensors, allocates the outputs that were not given, and calls the C ABI
+// on torch's current stream.  No step of a computation runs here.  These calls are
+// the short ones of a serving step, whose time on the host is what a caller without a
+// CUDA graph waits for; made through ctypes, a kv_append took 17 us there and
+// attn_fwd_tree 24.
+#include <ATen/core/Tensor.h>
+#include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/utils/pybind.h>
+
+#include <algorithm>
+#include <cmath>
+#include <climits>
+#include <initializer_list>
+#include <optional>
+#include <string>
+#include <tuple>
+
+#include "attn_bwd.h"
+#include "attn_fwd.h"
+#include "attn_kv.h"
+#include "attn_paged.h"
+
+namespace py = pybind11;
+using at::Tensor;
+using Maybe = std::optional<Tensor>;
+using Stream = std::optional<int64_t>;
+
+namespace {
+
+// Python's AttnError(status, message), handed over by ops.py (never freed: the module lives as long).
+PyObject* g_error_class = nullptr;
+
+void check(int status, const char* (*text)(int)) {
+  if (status == ATTN_OK) return;
+  PyErr_SetObject(g_error_class, py::make_tuple(status, text(status)).ptr());
+  throw py::error_already_set();
+}
+
+[[noreturn]] void refuse(const std::string& what) { throw py::value_error(what); }
+
+std::string shape_text(at::IntArrayRef shape) {
+  std::string s = "(";
+  for (size_t i = 0; i < shape.size(); ++i) s += (i ? ", " : "") + std::to_string(shape[i]);
+  return s + (shape.size() == 1 ? ",)" : ")");
+}
+
+struct Named {
+  const char* name;
+  const Tensor* t;
+  Named(const char* n, const Tensor& x) : name(n), t(&x) {}
+  Named(const char* n, const Maybe& x) : name(n), t(x ? &*x : nullptr) {}
+};
+
+// The index of the one CUDA device that the given tensors lie on, which has to be the current one.
+int common_device(std::initializer_list<Named> all) {
+  for (const Named& x : all)
+    if (x.t && !x.t->is_cuda()) refuse(std::string(x.name) + " must be a CUDA tensor");
+  const int current = c10::cuda::current_device();
+  for (const Named& x : all)
+    if (x.t && x.t->get_device() != current)
+      refuse(std::string(x.name) + " is on device " + std::to_string(x.t->get_device()) + ", the current device is " +
+             std::to_string(current));
+  return current;
+}
+
+cudaStream_t stream_of(const Stream& given, int device) {
+  if (given) return reinterpret_cast<cudaStream_t>(*given);
+  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+}
+
+Tensor empty(at::IntArrayRef shape, at::ScalarType type, int device) {
+  return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(device)));
+}
+
+void need(const char* name, const Tensor& t, at::ScalarType type, at::IntArrayRef shape) {
+  if (t.scalar_type() != type || t.sizes() != shape || !t.is_contiguous())
+    refuse(std::string(name) + " must be a contiguous " + c10::toString(type) + " tensor of shape " + shape_text(shape));
+}
+
+// The tensor given, or a new one.
+Tensor output(const char* name, const Maybe& given, at::ScalarType type, at::IntArrayRef shape, int device) {
+  if (!given) return empty(shape, type, device);
+  need(name, *given, type, shape);
+  return *given;
+}
+
+const int32_t* int32s(const char* name, const Tensor& t, int64_t n = -1) {
+  if (t.scalar_type() != at::kInt || t.dim() != 1 || !t.is_contiguous() || (n >= 0 && t.size(0) != n))
+    refuse(std::string(name) + " must be a contiguous int32 tensor [" + (n >= 0 ? std::to_string(n) : "n") + "]");
+  return t.const_data_ptr<int32_t>();
+}
+
+int as_int(const char* name, int64_t x) {
+  if (x < INT_MIN || x > INT_MAX) refuse(std::string(name) + " is beyond 32 bits");
+  return static_cast<int>(x);
+}
+
+int clamp_int(int64_t x) { return static_cast<int>(std::clamp<int64_t>(x, INT_MIN, INT_MAX)); }
+
+float scale_of(const std::optional<double>& scale, int64_t D) {
+  return static_cast<float>(scale ? *scale : 1.0 / std::sqrt(static_cast<double>(D)));
+}
+
+// ---------------------------------------------------------------------------- window
+struct Sizes {
+  int B, Hq, Hkv, Sq, Sk, D;
+};
+
+Sizes window_sizes(const Tensor& q, const Tensor& k, const Tensor& v, int64_t window, int64_t sinks, int64_t causal) {
+  for (const Named& x : {Named("q", q), Named("k", k), Named("v", v)})
+    if (x.t->scalar_type() != at::kBFloat16 || x.t->dim() != 4 || !x.t->is_contiguous())
+      refuse(std::string(x.name) + " must be a contiguous 4-d bf16 CUDA tensor");
+  if (v.sizes() != k.sizes() || k.size(0) != q.size(0) || k.size(3) != q.size(3))
+    refuse("shape mismatch q" + shape_text(q.sizes()) + " k" + shape_text(k.sizes()) + " v" + shape_text(v.sizes()));
+  if (causal != 1 && causal != 2) refuse("causal must be 1 (bottom-right) or 2 (top-left)");
+  if (window < 1 || sinks < 0) refuse("window must be at least 1 and sinks at least 0");
+  return {as_int("B", q.size(0)),  as_int("Hq", q.size(1)), as_int("Hkv", k.size(1)),
+          as_int("Sq", q.size(2)), as_int("Sk", k.size(2)), as_int("D", q.size(3))};
+}
+
+std::tuple<Tensor, Tensor> fwd_window(const Tensor& q, const Tensor& k, const Tensor& v, int64_t window, int64_t sinks,
+                                      int64_t causal, std::optional<double> scale, const Maybe& o, const Maybe& lse,
+                                      Stream stream) {
+  const int dev = common_device({{"q", q}, {"k", k}, {"v", v}, {"o", o}, {"lse", lse}});
+  const Sizes s = window_sizes(q, k, v, window, sinks, causal);
+  Tensor out = output("o", o, at::kBFloat16, q.sizes(), dev);
+  Tensor sums = output("lse", lse, at::kFloat, {s.B, s.Hq, s.Sq}, dev);
+  check(attn_fwd_window(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), out.mutable_data_ptr(),
+                        sums.mutable_data_ptr<float>(), s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, static_cast<int>(causal),
+                        clamp_int(window), clamp_int(sinks), scale_of(scale, s.D), stream_of(stream, dev)),
+        attn_fwd_strerror);
+  return {out, sums};
+}
+
+std::tuple<Tensor, Tensor, Tensor> bwd_window(const Tensor& q, const Tensor& k, const Tensor& v, const Tensor& o,
+                                              const Tensor& lse, const Tensor& dout, int64_t window, int64_t sinks,
+                                              int64_t causal, std::optional<double> scale, const Maybe& dq,
+                                              const Maybe& dk, const Maybe& dv, const Maybe& workspace, Stream stream) {
+  const std::initializer_list<Named> all = {{"q", q},   {"k", k},   {"v", v},   {"o", o},   {"lse", lse}, {"dout", dout},
+                                            {"dq", dq}, {"dk", dk}, {"dv", dv}, {"workspace", workspace}};
+  const int dev = common_device(all);
+  const Sizes s = window_sizes(q, k, v, window, sinks, causal);
+  need("o", o, at::kBFloat16, q.sizes());
+  need("dout", dout, at::kBFloat16, q.sizes());
+  need("lse", lse, at::kFloat, {s.B, s.Hq, s.Sq});
+  if (workspace && !workspace->is_contiguous()) refuse("workspace must be contiguous");
+  Tensor gq = output("dq", dq, at::kBFloat16, q.sizes(), dev);
+  Tensor gk = output("dk", dk, at::kBFloat16, k.sizes(), dev);
+  Tensor gv = output("dv", dv, at::kBFloat16, k.sizes(), dev);
+  const int w = clamp_int(window), n = clamp_int(sinks);
+  const size_t bytes = attn_bwd_window_workspace_size(s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, w, n);
+  Tensor ws = workspace ? *workspace : empty({static_cast<int64_t>(std::max<size_t>(bytes, 16))}, at::kByte, dev);
+  check(attn_bwd_window(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), o.const_data_ptr(),
+                        lse.const_data_ptr<float>(), dout.const_data_ptr(), gq.mutable_data_ptr(),
+                        gk.mutable_data_ptr(), gv.mutable_data_ptr(), s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D,
+                        static_cast<int>(causal), w, n, scale_of(scale, s.D), ws.mutable_data_ptr(), ws.nbytes(),
+                        stream_of(stream, dev)),
+        attn_bwd_strerror);
+  return {gq, gk, gv};
+}
+
+// ---------------------------------------------------------------------------- paged cache
+void put_rows(attn_kv_cache* c, const Tensor& page_table, const Tensor& seq_lens) {
+  if (page_table.scalar_type() != at::kInt || page_table.dim() != 2 || !page_table.is_contiguous())
+    refuse("page_table must be a contiguous int32 tensor [rows, max_pages]");
+  c->rows = as_int("rows", page_table.size(0));
+  c->max_pages = as_int("max_pages", page_table.size(1));
+  c->page_table = page_table.mutable_data_ptr<int32_t>();
+  c->seq_lens = const_cast<int32_t*>(int32s("seq_lens", seq_lens, c->rows));
+}
+
+attn_kv_cache cache_of(const Tensor& k, const Tensor& v, const Tensor& page_table, const Tensor& seq_lens,
+                       const Tensor* ref_counts) {
+  for (const Named& x : {Named("k_pages", k), Named("v_pages", v)})
+    if (x.t->scalar_type() != at::kBFloat16 || x.t->dim() != 4 || x.t->stride(3) != 1)
+      refuse(std::string(x.name) + " must be a bf16 tensor [pages, Hkv, page_size, D] whose last stride is 1");
+  if (v.sizes() != k.sizes())
+    refuse("shape mismatch k_pages" + shape_text(k.sizes()) + " v_pages" + shape_text(v.sizes()));
+  attn_kv_cache c{};
+  c.k = k.mutable_data_ptr();
+  c.v = v.mutable_data_ptr();
+  c.k_stride_page = k.stride(0);
+  c.k_stride_head = k.stride(1);
+  c.k_stride_slot = k.stride(2);
+  c.v_stride_page = v.stride(0);
+  c.v_stride_head = v.stride(1);
+  c.v_stride_slot = v.stride(2);
+  c.n_pages = as_int("pages", k.size(0));
+  c.Hkv = as_int("Hkv", k.size(1));
+  c.page_size = as_int("page_size", k.size(2));
+  c.D = as_int("D", k.size(3));
+  put_rows(&c, page_table, seq_lens);
+  if (ref_counts) c.ref_counts = const_cast<int32_t*>(int32s("ref_counts", *ref_counts, c.n_pages));
+  return c;
+}
+
+std::tuple<Tensor, Tensor> fwd_tree(const Tensor& q, const Tensor& k_pages, const Tensor& v_pages,
+                                    const Tensor& page_table, const Tensor& seq_lens, const Tensor& cu_tokens,
+                                    const Maybe& tree_mask, int64_t window, int64_t sinks, std::optional<double> scale,
+                                    const Maybe& o, const Maybe& lse, const Maybe& workspace, Stream stream) {
+  const std::initializer_list<Named> all = {{"q", q},
+                                            {"k_pages", k_pages},
+                                            {"v_pages", v_pages},
+                                            {"page_table", page_table},
+                                            {"seq_lens", seq_lens},
+                                            {"cu_tokens", cu_tokens},
+                                            {"tree_mask", tree_mask},
+                                            {"o", o},
+                                            {"lse", lse},
+                                            {"workspace", workspace}};
+  const int dev = common_device(all);
+  const attn_kv_cache c = cache_of(k_pages, v_pages, page_table, seq_lens, nullptr);
+  if (q.scalar_type() != at::kBFloat16 || q.dim() != 3 || q.size(2) != c.D || q.stride(2) != 1)
+    refuse("q must be a bf16 tensor [tokens, Hq, " + std::to_string(c.D) + "] whose last stride is 1");
+  const int T = as_int("tokens", q.size(0)), Hq = as_int("Hq", q.size(1));
+  const int32_t* cu = int32s("cu_tokens", cu_tokens, static_cast<int64_t>(c.rows) + 1);
+  const uint32_t* mask = nullptr;
+  int words = 0;
+  if (tree_mask) {
+    if (tree_mask->element_size() != 4 || tree_mask->dim() != 2 || tree_mask->size(0) != T ||
+        !tree_mask->is_contiguous())
+      refuse("tree_mask must be a contiguous 32-bit tensor [" + std::to_string(T) + ", words]");
+    words = as_int("words", tree_mask->size(1));
+    mask = static_cast<const uint32_t*>(tree_mask->const_data_ptr());
+  }
+  if (workspace && !workspace->is_contiguous()) refuse("workspace must be contiguous");
+  Tensor out = output("o", o, at::kBFloat16, {T, Hq, c.D}, dev);
+  Tensor sums = output("lse", lse, at::kFloat, {T, Hq}, dev);
+  Tensor ws = workspace ? *workspace
+                        : empty({static_cast<int64_t>(attn_fwd_tree_workspace_size(c.D))}, at::kByte, dev);
+  check(attn_fwd_tree(&c, q.const_data_ptr(), q.stride(0), q.stride(1), out.mutable_data_ptr(),
+                      sums.mutable_data_ptr<float>(), T, Hq, cu, mask, words, clamp_int(window), clamp_int(sinks),
+                      scale_of(scale, c.D), ws.mutable_data_ptr(), ws.nbytes(), stream_of(stream, dev)),
+        attn_paged_strerror);
+  return {out, sums};
+}
+
+Tensor kv_append(const Tensor& k_new, const Tensor& v_new, const Tensor& k_pages, const Tensor& v_pages,
+                 const Tensor& page_table, const Tensor& seq_lens, const Tensor& ref_counts, const Tensor& cu_tokens,
+                 const Maybe& status, Stream stream) {
+  const std::initializer_list<Named> all = {{"k_new", k_new},           {"v_new", v_new},       {"k_pages", k_pages},
+                                            {"v_pages", v_pages},       {"page_table", page_table}, {"seq_lens", seq_lens},
+                                            {"ref_counts", ref_counts}, {"cu_tokens", cu_tokens}, {"status", status}};
+  const int dev = common_device(all);
+  const attn_kv_cache c = cache_of(k_pages, v_pages, page_table, seq_lens, &ref_counts);
+  for (const Named& x : {Named("k_new", k_new), Named("v_new", v_new)})
+    if (x.t->scalar_type() != at::kBFloat16 || x.t->dim() != 3 || x.t->size(1) != c.Hkv || x.t->size(2) != c.D ||
+        x.t->stride(2) != 1)
+      refuse(std::string(x.name) + " must be a bf16 tensor [tokens, " + std::to_string(c.Hkv) + ", " +
+             std::to_string(c.D) + "] whose last stride is 1");
+  if (v_new.size(0) != k_new.size(0))
+    refuse("shape mismatch k_new" + shape_text(k_new.sizes()) + " v_new" + shape_text(v_new.sizes()));
+  const int32_t* cu = int32s("cu_tokens", cu_tokens, static_cast<int64_t>(c.rows) + 1);
+  Tensor done = output("status", status, at::kInt, {1}, dev);
+  check(attn_kv_append(&c, k_new.const_data_ptr(), v_new.const_data_ptr(), k_new.stride(0), k_new.stride(1),
+                       v_new.stride(0), v_new.stride(1), as_int("tokens", k_new.size(0)), cu,
+                       done.mutable_data_ptr<int32_t>(), stream_of(stream, dev)),
+        attn_kv_strerror);
+  return done;
+}
+
+Tensor kv_fork(const Tensor& k_pages, const Tensor& v_pages, const Tensor& page_table, const Tensor& seq_lens,
+               const Tensor& ref_counts, const Tensor& parents, const Tensor& children, const Maybe& status,
+               Stream stream) {
+  const std::initializer_list<Named> all = {{"k_pages", k_pages},       {"v_pages", v_pages}, {"page_table", page_table},
+                                            {"seq_lens", seq_lens},     {"ref_counts", ref_counts}, {"parents", parents},
+                                            {"children", children},     {"status", status}};
+  const int dev = common_device(all);
+  const attn_kv_cache c = cache_of(k_pages, v_pages, page_table, seq_lens, &ref_counts);
+  const int32_t* from = int32s("parents", parents);
+  const int32_t* to = int32s("children", children, parents.size(0));
+  Tensor done = output("status", status, at::kInt, {1}, dev);
+  check(attn_kv_fork(&c, from, to, as_int("parents", parents.size(0)), done.mutable_data_ptr<int32_t>(),
+                     stream_of(stream, dev)),
+        attn_kv_strerror);
+  return done;
+}
+
+Tensor kv_compact(const Tensor& k_pages, const Tensor& v_pages, const Tensor& page_table, const Tensor& seq_lens,
+                  const Tensor& ref_counts, const Tensor& cu_tokens, const Tensor& accepted, const Tensor& cu_accepted,
+                  const Maybe& status, Stream stream) {
+  const std::initializer_list<Named> all = {{"k_pages", k_pages},         {"v_pages", v_pages},
+                                            {"page_table", page_table},   {"seq_lens", seq_lens},
+                                            {"ref_counts", ref_counts},   {"cu_tokens", cu_tokens},
+                                            {"accepted", accepted},       {"cu_accepted", cu_accepted},
+                                            {"status", status}};
+  const int dev = common_device(all);
+  const attn_kv_cache c = cache_of(k_pages, v_pages, page_table, seq_lens, &ref_counts);
+  const int64_t ends = static_cast<int64_t>(c.rows) + 1;
+  const int32_t* cu = int32s("cu_tokens", cu_tokens, ends);
+  const int32_t* cu_acc = int32s("cu_accepted", cu_accepted, ends);
+  const int32_t* acc = int32s("accepted", accepted);
+  Tensor done = output("status", status, at::kInt, {c.rows}, dev);
+  check(attn_kv_compact(&c, cu, acc, as_int("accepted", accepted.size(0)), cu_acc, done.mutable_data_ptr<int32_t>(),
+                        stream_of(stream, dev)),
+        attn_kv_strerror);
+  return done;
+}
+
+void kv_free(const Tensor& page_table, const Tensor& seq_lens, const Tensor& ref_counts, const Tensor& rows,
+             int64_t page_size, Stream stream) {
+  const std::initializer_list<Named> all = {
+      {"page_table", page_table}, {"seq_lens", seq_lens}, {"ref_counts", ref_counts}, {"rows", rows}};
+  const int dev = common_device(all);
+  attn_kv_cache c{};
+  put_rows(&c, page_table, seq_lens);
+  c.ref_counts = const_cast<int32_t*>(int32s("ref_counts", ref_counts));
+  c.n_pages = as_int("pages", ref_counts.size(0));
+  c.page_size = clamp_int(page_size);
+  c.Hkv = 1;  // heads and D are not used
+  c.D = 64;
+  const int32_t* list = int32s("rows", rows);
+  check(attn_kv_free(&c, list, as_int("rows", rows.size(0)), stream_of(stream, dev)), attn_kv_strerror);
+}
+
+}  // namespace
+
+PYBIND11_MODULE(attn_binding, m) {
+  m.def("set_error_class", [](py::object cls) { g_error_class = cls.release().ptr(); });
+  m.def("fwd_window", &fwd_window);
+  m.def("bwd_window", &bwd_window);
+  m.def("fwd_tree", &fwd_tree);
+  m.def("kv_append", &kv_append);
+  m.def("kv_fork", &kv_fork);
+  m.def("kv_compact", &kv_compact);
+  m.def("kv_free", &kv_free);
+}

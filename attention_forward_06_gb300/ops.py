@@ -1,16 +1,17 @@
-"""Python binding of the C ABI (include/attn_fwd.h): marshals torch tensors into
-pointers and sizes and calls the CUDA library.  Every step of the attention
-computation runs in the library's kernel; torch only provides device memory and
-streams here.
+"""Python binding of the C ABI (include/attn_fwd.h, attn_bwd.h, attn_kv.h,
+attn_paged.h): marshals torch tensors into pointers and sizes and calls the CUDA
+libraries.  Every step of the computation runs in their kernels; torch only
+provides device memory and streams here.  The window, paged and cache calls are
+marshalled in C++ (csrc/binding.cpp), the others here.
 """
 from __future__ import annotations
 
 import ctypes
 import math
-import struct
 
 import torch
 
+from . import _lib
 from ._lib import load
 
 ATTN_OK = 0
@@ -239,45 +240,16 @@ def attn_fwd_ordered(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, tile_ord
     return o, lse
 
 
-def _on_device(**tensors) -> int:
-    """The index of the one CUDA device that all of the given tensors (None: absent) lie on, which has to be the
-    current one."""
-    index = -1
-    for t in tensors.values():
-        if t is not None:
-            i = t.get_device()
-            if index < 0:
-                index = i
-            if i < 0 or i != index:
-                break
-    else:
-        if index == torch.cuda.current_device():
-            return index
-    for name, t in tensors.items():
-        if t is not None and not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
-    raise ValueError("the tensors have to be on the current device: " +
-                     ", ".join(f"{name} is on {t.device}" for name, t in tensors.items() if t is not None))
+def _binding():
+    m = _lib._binding
+    if m is None:
+        m = _lib.binding()
+        m.set_error_class(AttnError)
+    return m
 
 
-def _is(t: torch.Tensor, dtype: torch.dtype, shape) -> bool:
-    """A contiguous tensor of this type and shape?"""
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
-
-
-def _window_shapes(q, k, v, window, sinks, causal):
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if t.dtype is not torch.bfloat16 or t.dim() != 4 or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 4-d bf16 CUDA tensor")
-    B, Hq, Sq, D = q.shape
-    Bk, Hkv, Sk, Dk = k.shape
-    if v.shape != k.shape or Bk != B or Dk != D:
-        raise ValueError(f"shape mismatch q{tuple(q.shape)} k{tuple(k.shape)} v{tuple(v.shape)}")
-    if causal not in (1, 2):
-        raise ValueError("causal must be 1 (bottom-right) or 2 (top-left)")
-    if window < 1 or sinks < 0:
-        raise ValueError("window must be at least 1 and sinks at least 0")
-    return B, Hq, Hkv, Sq, Sk, D
+def _handle(stream) -> int | None:
+    return None if stream is None else _stream_handle(stream)
 
 
 _INT_MAX = 2 ** 31 - 1
@@ -291,22 +263,7 @@ def attn_fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: i
     ``attn_fwd`` with key j visible to row i iff ``j <= p_i`` and (``p_i - j < window`` or ``j < sinks``), where
     ``p_i`` is ``i + Sk - Sq`` (causal 1) or ``i`` (causal 2).  A row without keys gets ``o = 0``, ``lse = -inf``.
     """
-    B, Hq, Hkv, Sq, Sk, D = _window_shapes(q, k, v, window, sinks, causal)
-    device = _on_device(q=q, k=k, v=v, o=o, lse=lse)
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    if o is None:
-        o = torch.empty_like(q)
-    elif not _is(o, torch.bfloat16, q.shape):
-        raise ValueError("o must be a contiguous bf16 tensor shaped like q")
-    if lse is None:
-        lse = torch.empty((B, Hq, Sq), dtype=torch.float32, device=device)
-    elif not _is(lse, torch.float32, (B, Hq, Sq)):
-        raise ValueError("lse must be a contiguous fp32 tensor [B, Hq, Sq]")
-    _check(load().attn_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv,
-                                  Sq, Sk, D, int(causal), min(int(window), _INT_MAX), min(int(sinks), _INT_MAX),
-                                  float(scale), _stream_handle(stream)))
-    return o, lse
+    return _binding().fwd_window(q, k, v, window, sinks, causal, scale, o, lse, _handle(stream))
 
 
 def bwd_workspace_size(B: int, Hq: int, Sq: int) -> int:
@@ -363,83 +320,11 @@ def attn_bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.
     ``workspace`` (a contiguous CUDA tensor of at least ``bwd_window_workspace_size`` bytes) is allocated here
     when not given.
     """
-    B, Hq, Hkv, Sq, Sk, D = _window_shapes(q, k, v, window, sinks, causal)
-    device = _on_device(q=q, k=k, v=v, o=o, lse=lse, dout=dout, dq=dq, dk=dk, dv=dv, workspace=workspace)
-    for name, t, like in (("o", o, q), ("dout", dout, q), ("dq", dq, q), ("dk", dk, k), ("dv", dv, k)):
-        if t is not None and not _is(t, torch.bfloat16, like.shape):
-            raise ValueError(f"{name} must be a contiguous bf16 tensor of shape {tuple(like.shape)}")
-    if not _is(lse, torch.float32, (B, Hq, Sq)):
-        raise ValueError("lse must be the forward's contiguous fp32 [B, Hq, Sq]")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
-    if workspace is None:
-        need = bwd_window_workspace_size(B, Hq, Hkv, Sq, Sk, D, window, sinks)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    lib = load("attn_bwd")
-    st = lib.attn_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), dout.data_ptr(),
-                             dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Sq, Sk, D, int(causal),
-                             min(int(window), _INT_MAX), min(int(sinks), _INT_MAX), float(scale),
-                             workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                             _stream_handle(stream))
-    if st != ATTN_OK:
-        raise AttnError(st, lib.attn_bwd_strerror(st).decode())
-    return dq, dk, dv
+    return _binding().bwd_window(q, k, v, o, lse, dout, window, sinks, causal, scale, dq, dk, dv, workspace,
+                                 _handle(stream))
 
 
 KV_INVALID = -1  # device status: lengths, indices or lists that do not fit each other (ATTN_KV_INVALID)
-
-
-def _int32(name: str, t: torch.Tensor, n: int | None = None) -> torch.Tensor:
-    """``t``, which has to be a contiguous int32 vector (of n entries)."""
-    if t.dtype is not torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be a contiguous int32 tensor [{'n' if n is None else n}]")
-    return t
-
-
-_pack_cache = struct.Struct("2P6q3P6i").pack  # attn_kv_cache (include/attn_kv.h)
-
-
-def _page_table(page_table, seq_lens) -> tuple[int, int]:
-    if page_table.dtype is not torch.int32 or page_table.dim() != 2 or not page_table.is_contiguous():
-        raise ValueError("page_table must be a contiguous int32 tensor [rows, max_pages]")
-    rows, max_pages = page_table.shape
-    _int32("seq_lens", seq_lens, rows)
-    return rows, max_pages
-
-
-def _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts=None):
-    """The C ABI's cache of ``k_pages``/``v_pages [pages, Hkv, page_size, D]`` (any strides but the last, 1), and
-    ``rows, Hkv, D``."""
-    shape, (kp, kh, ks, k1), (vp, vh, vs, v1) = k_pages.shape, _strides(k_pages), _strides(v_pages)
-    if k_pages.dtype is not torch.bfloat16 or v_pages.dtype is not torch.bfloat16 or k1 != 1 or v1 != 1:
-        raise ValueError("k_pages and v_pages must be bf16 tensors [pages, Hkv, page_size, D] whose last stride is 1")
-    if v_pages.shape != shape:
-        raise ValueError(f"shape mismatch k_pages{tuple(shape)} v_pages{tuple(v_pages.shape)}")
-    n_pages, Hkv, page_size, D = shape
-    rows, max_pages = _page_table(page_table, seq_lens)
-    refs = _int32("ref_counts", ref_counts, n_pages).data_ptr() if ref_counts is not None else 0
-    return _pack_cache(k_pages.data_ptr(), v_pages.data_ptr(), kp, kh, ks, vp, vh, vs, page_table.data_ptr(),
-                       seq_lens.data_ptr(), refs, n_pages, Hkv, page_size, D, rows, max_pages), rows, Hkv, D
-
-
-def _strides(pages) -> tuple:
-    if pages.dim() != 4:
-        raise ValueError("k_pages and v_pages must be 4-d tensors [pages, Hkv, page_size, D]")
-    return pages.stride()
-
-
-def _check_kv(status: int) -> None:
-    if status != ATTN_OK:
-        raise AttnError(status, load("attn_kv").attn_kv_strerror(status).decode())
-
-
-def _status(status, n: int, device: int) -> torch.Tensor:
-    return torch.empty(n, dtype=torch.int32, device=device) if status is None else _int32("status", status, n)
 
 
 def kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -451,19 +336,8 @@ def kv_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor, v
     behind its ``seq_lens[b]`` tokens, which grow; pages are taken as they are needed.  ``status`` is 0, the number
     of pages missing, or ``KV_INVALID``; unless it is 0 nothing has changed.  Nothing waits for the device.
     """
-    dev = _on_device(k_pages=k_pages, v_pages=v_pages, k_new=k_new, v_new=v_new, page_table=page_table,
-                     seq_lens=seq_lens, ref_counts=ref_counts, cu_tokens=cu_tokens, status=status)
-    cache, rows, Hkv, D = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
-    n = k_new.shape[0]
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.dtype is not torch.bfloat16 or t.shape != (n, Hkv, D) or t.stride(2) != 1:
-            raise ValueError(f"{name} must be a bf16 tensor [{n}, {Hkv}, {D}] whose last stride is 1")
-    _int32("cu_tokens", cu_tokens, rows + 1)
-    status = _status(status, 1, dev)
-    _check_kv(load("attn_kv").attn_kv_append(cache, k_new.data_ptr(), v_new.data_ptr(), *k_new.stride()[:2],
-                                             *v_new.stride()[:2], n, cu_tokens.data_ptr(),
-                                             status.data_ptr(), _stream_handle(stream)))
-    return status
+    return _binding().kv_append(k_new, v_new, k_pages, v_pages, page_table, seq_lens, ref_counts, cu_tokens, status,
+                                _handle(stream))
 
 
 def kv_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -473,15 +347,8 @@ def kv_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tens
 
     Full pages are shared, a partly filled last page is copied.  ``status`` as ``kv_append``'s.
     """
-    dev = _on_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
-                     ref_counts=ref_counts, parents=parents, children=children, status=status)
-    cache = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)[0]
-    n = _int32("parents", parents).shape[0]
-    _int32("children", children, n)
-    status = _status(status, 1, dev)
-    _check_kv(load("attn_kv").attn_kv_fork(cache, parents.data_ptr(), children.data_ptr(), n, status.data_ptr(),
-                                           _stream_handle(stream)))
-    return status
+    return _binding().kv_fork(k_pages, v_pages, page_table, seq_lens, ref_counts, parents, children, status,
+                              _handle(stream))
 
 
 def kv_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -493,17 +360,8 @@ def kv_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, page_table: torch.T
     cu_accepted[b+1]]`` lists (ascending) move together, the others are dropped and pages past the end are given
     back.  ``status[b]`` is 0, or ``KV_INVALID`` for a row that is left as it was.
     """
-    dev = _on_device(k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
-                     ref_counts=ref_counts, cu_tokens=cu_tokens, accepted=accepted, cu_accepted=cu_accepted,
-                     status=status)
-    cache, rows, _, _ = _kv_cache(k_pages, v_pages, page_table, seq_lens, ref_counts)
-    _int32("cu_tokens", cu_tokens, rows + 1)
-    _int32("cu_accepted", cu_accepted, rows + 1)
-    _int32("accepted", accepted)
-    status = _status(status, rows, dev)
-    _check_kv(load("attn_kv").attn_kv_compact(cache, cu_tokens.data_ptr(), accepted.data_ptr(), accepted.shape[0],
-                                              cu_accepted.data_ptr(), status.data_ptr(), _stream_handle(stream)))
-    return status
+    return _binding().kv_compact(k_pages, v_pages, page_table, seq_lens, ref_counts, cu_tokens, accepted, cu_accepted,
+                                 status, _handle(stream))
 
 
 def kv_free(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.Tensor, rows: torch.Tensor,
@@ -512,13 +370,7 @@ def kv_free(page_table: torch.Tensor, seq_lens: torch.Tensor, ref_counts: torch.
 
     A row listed twice is freed once; one that is out of range is passed over.
     """
-    _on_device(page_table=page_table, seq_lens=seq_lens, ref_counts=ref_counts, rows=rows)
-    n_rows, max_pages = _page_table(page_table, seq_lens)
-    n_pages = _int32("ref_counts", ref_counts).shape[0]
-    n = _int32("rows", rows).shape[0]
-    cache = _pack_cache(0, 0, 0, 0, 0, 0, 0, 0, page_table.data_ptr(), seq_lens.data_ptr(), ref_counts.data_ptr(),
-                        n_pages, 1, int(page_size), 64, n_rows, max_pages)  # heads and D are not used
-    _check_kv(load("attn_kv").attn_kv_free(cache, rows.data_ptr(), n, _stream_handle(stream)))
+    _binding().kv_free(page_table, seq_lens, ref_counts, rows, page_size, _handle(stream))
 
 
 def pack_tree_mask(visible: torch.Tensor) -> torch.Tensor:
@@ -550,44 +402,8 @@ def attn_fwd_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
     ``window > 0`` keeps keys nearer than that and the first ``sinks``.  Tokens of no row keep what ``o`` and ``lse``
     hold.  ``workspace`` (contiguous, ``tree_workspace_size`` bytes) is allocated here when not given.
     """
-    dev = _on_device(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, seq_lens=seq_lens,
-                     cu_tokens=cu_tokens, tree_mask=tree_mask, o=o, lse=lse, workspace=workspace)
-    cache, rows, _, D = _kv_cache(k_pages, v_pages, page_table, seq_lens)
-    if q.dtype is not torch.bfloat16 or q.dim() != 3:
-        raise ValueError(f"q must be a bf16 tensor [tokens, Hq, {D}] whose last stride is 1")
-    T, Hq, Dq = q.shape
-    q_token, q_head, q_last = q.stride()
-    if Dq != D or q_last != 1:
-        raise ValueError(f"q must be a bf16 tensor [tokens, Hq, {D}] whose last stride is 1")
-    _int32("cu_tokens", cu_tokens, rows + 1)
-    words = 0
-    if tree_mask is not None:
-        if tree_mask.element_size() != 4 or tree_mask.dim() != 2 or tree_mask.shape[0] != T or \
-                not tree_mask.is_contiguous():
-            raise ValueError(f"tree_mask must be a contiguous 32-bit tensor [{T}, words]")
-        words = tree_mask.shape[1]
-    if o is None:
-        o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev)
-    elif not _is(o, torch.bfloat16, (T, Hq, D)):
-        raise ValueError("o must be a contiguous bf16 tensor shaped like q")
-    if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-    elif not _is(lse, torch.float32, (T, Hq)):
-        raise ValueError("lse must be a contiguous fp32 tensor [tokens, Hq]")
-    lib = load("attn_paged")
-    if workspace is None:
-        workspace = torch.empty(lib.attn_fwd_tree_workspace_size(D), dtype=torch.uint8, device=dev)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    if scale is None:
-        scale = 1.0 / math.sqrt(D)
-    st = lib.attn_fwd_tree(cache, q.data_ptr(), q_token, q_head, o.data_ptr(), lse.data_ptr(), T, Hq,
-                           cu_tokens.data_ptr(), tree_mask.data_ptr() if tree_mask is not None else None, words,
-                           min(int(window), _INT_MAX), min(int(sinks), _INT_MAX), float(scale), workspace.data_ptr(),
-                           workspace.numel() * workspace.element_size(), _stream_handle(stream))
-    if st != ATTN_OK:
-        raise AttnError(st, lib.attn_paged_strerror(st).decode())
-    return o, lse
+    return _binding().fwd_tree(q, k_pages, v_pages, page_table, seq_lens, cu_tokens, tree_mask, window, sinks, scale, o,
+                               lse, workspace, _handle(stream))
 
 
 def paged_debug_status(stream=None) -> tuple[int, int]:
