@@ -1324,14 +1324,9 @@ Workspace layout(int D) {
   return w;
 }
 
-bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
-  if (!a || !b || na == 0 || nb == 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
-  return a0 < b0 + nb && b0 < a0 + na;
-}
-
 template <int D>
-int launch(const QMaps& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int sms, cudaStream_t stream) {
+int launch(const QMaps& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int sms,
+           cudaStream_t stream) {
   const int grid = std::min(sms, kMaxCtas);
   if (p.item_tokens > p.R)
     attn_tree_kernel<D, true><<<grid, kThreads, Cfg<D, true>::kSmemBytes, stream>>>(tq, tk, tv, p);
@@ -1401,9 +1396,9 @@ int attn_fwd_tree(const attn_kv_cache* cache, const void* q, int64_t q_stride_to
              {tree_mask, static_cast<size_t>(n_tokens) * mask_words * 4}};
   for (int a = 0; a < 3; ++a) {
     for (const auto& in : ins)
-      if (overlaps(outs[a].at, outs[a].bytes, in.at, in.bytes)) return ATTN_ERR_INVALID_ARG;
+      if (attn_host::overlap(outs[a].at, outs[a].bytes, in.at, in.bytes)) return ATTN_ERR_INVALID_ARG;
     for (int b = a + 1; b < 3; ++b)
-      if (overlaps(outs[a].at, outs[a].bytes, outs[b].at, outs[b].bytes)) return ATTN_ERR_INVALID_ARG;
+      if (attn_host::overlap(outs[a].at, outs[a].bytes, outs[b].at, outs[b].bytes)) return ATTN_ERR_INVALID_ARG;
   }
 
   // ---- device

@@ -7,6 +7,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/utils/pybind.h>
 
@@ -66,10 +67,26 @@ int common_device(std::initializer_list<Named> all) {
   return current;
 }
 
-cudaStream_t stream_of(const Stream& given, int device) {
-  if (given) return reinterpret_cast<cudaStream_t>(*given);
-  return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
-}
+// The stream of a call: torch's current one, or the one given, which is then the current one until the
+// call returns, so that what is allocated here belongs to it (a workspace freed on return is not handed
+// to another stream's work while the kernels run).
+class OnStream {
+ public:
+  OnStream(const Stream& given, int device) {
+    const auto index = static_cast<c10::DeviceIndex>(device);
+    if (given) {
+      stream_ = reinterpret_cast<cudaStream_t>(*given);
+      guard_.reset_stream(c10::cuda::getStreamFromExternal(stream_, index).unwrap());
+    } else {
+      stream_ = c10::cuda::getCurrentCUDAStream(index).stream();
+    }
+  }
+  operator cudaStream_t() const { return stream_; }
+
+ private:
+  cudaStream_t stream_;
+  c10::cuda::OptionalCUDAStreamGuard guard_;
+};
 
 Tensor empty(at::IntArrayRef shape, at::ScalarType type, int device) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(at::kCUDA, static_cast<c10::DeviceIndex>(device)));
@@ -77,7 +94,8 @@ Tensor empty(at::IntArrayRef shape, at::ScalarType type, int device) {
 
 void need(const char* name, const Tensor& t, at::ScalarType type, at::IntArrayRef shape) {
   if (t.scalar_type() != type || t.sizes() != shape || !t.is_contiguous())
-    refuse(std::string(name) + " must be a contiguous " + c10::toString(type) + " tensor of shape " + shape_text(shape));
+    refuse(std::string(name) + " must be a contiguous " + c10::toString(type) + " tensor of shape " +
+           shape_text(shape));
 }
 
 // The tensor given, or a new one.
@@ -125,12 +143,13 @@ std::tuple<Tensor, Tensor> fwd_window(const Tensor& q, const Tensor& k, const Te
                                       int64_t causal, std::optional<double> scale, const Maybe& o, const Maybe& lse,
                                       Stream stream) {
   const int dev = common_device({{"q", q}, {"k", k}, {"v", v}, {"o", o}, {"lse", lse}});
+  const OnStream on(stream, dev);
   const Sizes s = window_sizes(q, k, v, window, sinks, causal);
   Tensor out = output("o", o, at::kBFloat16, q.sizes(), dev);
   Tensor sums = output("lse", lse, at::kFloat, {s.B, s.Hq, s.Sq}, dev);
   check(attn_fwd_window(q.const_data_ptr(), k.const_data_ptr(), v.const_data_ptr(), out.mutable_data_ptr(),
                         sums.mutable_data_ptr<float>(), s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D, static_cast<int>(causal),
-                        clamp_int(window), clamp_int(sinks), scale_of(scale, s.D), stream_of(stream, dev)),
+                        clamp_int(window), clamp_int(sinks), scale_of(scale, s.D), on),
         attn_fwd_strerror);
   return {out, sums};
 }
@@ -142,6 +161,7 @@ std::tuple<Tensor, Tensor, Tensor> bwd_window(const Tensor& q, const Tensor& k, 
   const std::initializer_list<Named> all = {{"q", q},   {"k", k},   {"v", v},   {"o", o},   {"lse", lse}, {"dout", dout},
                                             {"dq", dq}, {"dk", dk}, {"dv", dv}, {"workspace", workspace}};
   const int dev = common_device(all);
+  const OnStream on(stream, dev);
   const Sizes s = window_sizes(q, k, v, window, sinks, causal);
   need("o", o, at::kBFloat16, q.sizes());
   need("dout", dout, at::kBFloat16, q.sizes());
@@ -157,7 +177,7 @@ std::tuple<Tensor, Tensor, Tensor> bwd_window(const Tensor& q, const Tensor& k, 
                         lse.const_data_ptr<float>(), dout.const_data_ptr(), gq.mutable_data_ptr(),
                         gk.mutable_data_ptr(), gv.mutable_data_ptr(), s.B, s.Hq, s.Hkv, s.Sq, s.Sk, s.D,
                         static_cast<int>(causal), w, n, scale_of(scale, s.D), ws.mutable_data_ptr(), ws.nbytes(),
-                        stream_of(stream, dev)),
+                        on),
         attn_bwd_strerror);
   return {gq, gk, gv};
 }
@@ -212,6 +232,7 @@ std::tuple<Tensor, Tensor> fwd_tree(const Tensor& q, const Tensor& k_pages, cons
                                             {"lse", lse},
                                             {"workspace", workspace}};
   const int dev = common_device(all);
+  const OnStream on(stream, dev);
   const attn_kv_cache c = cache_of(k_pages, v_pages, page_table, seq_lens, nullptr);
   if (q.scalar_type() != at::kBFloat16 || q.dim() != 3 || q.size(2) != c.D || q.stride(2) != 1)
     refuse("q must be a bf16 tensor [tokens, Hq, " + std::to_string(c.D) + "] whose last stride is 1");
@@ -223,7 +244,8 @@ std::tuple<Tensor, Tensor> fwd_tree(const Tensor& q, const Tensor& k_pages, cons
     if (tree_mask->element_size() != 4 || tree_mask->dim() != 2 || tree_mask->size(0) != T ||
         !tree_mask->is_contiguous())
       refuse("tree_mask must be a contiguous 32-bit tensor [" + std::to_string(T) + ", words]");
-    words = as_int("words", tree_mask->size(1));
+    if (tree_mask->size(1) < 1) refuse("tree_mask must have a word at least");
+    words = T > 0 ? as_int("words", tree_mask->size(1)) : 0;
     mask = static_cast<const uint32_t*>(tree_mask->const_data_ptr());
   }
   if (workspace && !workspace->is_contiguous()) refuse("workspace must be contiguous");
@@ -233,7 +255,7 @@ std::tuple<Tensor, Tensor> fwd_tree(const Tensor& q, const Tensor& k_pages, cons
                         : empty({static_cast<int64_t>(attn_fwd_tree_workspace_size(c.D))}, at::kByte, dev);
   check(attn_fwd_tree(&c, q.const_data_ptr(), q.stride(0), q.stride(1), out.mutable_data_ptr(),
                       sums.mutable_data_ptr<float>(), T, Hq, cu, mask, words, clamp_int(window), clamp_int(sinks),
-                      scale_of(scale, c.D), ws.mutable_data_ptr(), ws.nbytes(), stream_of(stream, dev)),
+                      scale_of(scale, c.D), ws.mutable_data_ptr(), ws.nbytes(), on),
         attn_paged_strerror);
   return {out, sums};
 }
@@ -245,6 +267,7 @@ Tensor kv_append(const Tensor& k_new, const Tensor& v_new, const Tensor& k_pages
                                             {"v_pages", v_pages},       {"page_table", page_table}, {"seq_lens", seq_lens},
                                             {"ref_counts", ref_counts}, {"cu_tokens", cu_tokens}, {"status", status}};
   const int dev = common_device(all);
+  const OnStream on(stream, dev);
   const attn_kv_cache c = cache_of(k_pages, v_pages, page_table, seq_lens, &ref_counts);
   for (const Named& x : {Named("k_new", k_new), Named("v_new", v_new)})
     if (x.t->scalar_type() != at::kBFloat16 || x.t->dim() != 3 || x.t->size(1) != c.Hkv || x.t->size(2) != c.D ||
@@ -257,7 +280,7 @@ Tensor kv_append(const Tensor& k_new, const Tensor& v_new, const Tensor& k_pages
   Tensor done = output("status", status, at::kInt, {1}, dev);
   check(attn_kv_append(&c, k_new.const_data_ptr(), v_new.const_data_ptr(), k_new.stride(0), k_new.stride(1),
                        v_new.stride(0), v_new.stride(1), as_int("tokens", k_new.size(0)), cu,
-                       done.mutable_data_ptr<int32_t>(), stream_of(stream, dev)),
+                       done.mutable_data_ptr<int32_t>(), on),
         attn_kv_strerror);
   return done;
 }
@@ -269,12 +292,13 @@ Tensor kv_fork(const Tensor& k_pages, const Tensor& v_pages, const Tensor& page_
                                             {"seq_lens", seq_lens},     {"ref_counts", ref_counts}, {"parents", parents},
                                             {"children", children},     {"status", status}};
   const int dev = common_device(all);
+  const OnStream on(stream, dev);
   const attn_kv_cache c = cache_of(k_pages, v_pages, page_table, seq_lens, &ref_counts);
   const int32_t* from = int32s("parents", parents);
   const int32_t* to = int32s("children", children, parents.size(0));
   Tensor done = output("status", status, at::kInt, {1}, dev);
   check(attn_kv_fork(&c, from, to, as_int("parents", parents.size(0)), done.mutable_data_ptr<int32_t>(),
-                     stream_of(stream, dev)),
+                     on),
         attn_kv_strerror);
   return done;
 }
@@ -288,6 +312,7 @@ Tensor kv_compact(const Tensor& k_pages, const Tensor& v_pages, const Tensor& pa
                                             {"accepted", accepted},       {"cu_accepted", cu_accepted},
                                             {"status", status}};
   const int dev = common_device(all);
+  const OnStream on(stream, dev);
   const attn_kv_cache c = cache_of(k_pages, v_pages, page_table, seq_lens, &ref_counts);
   const int64_t ends = static_cast<int64_t>(c.rows) + 1;
   const int32_t* cu = int32s("cu_tokens", cu_tokens, ends);
@@ -295,7 +320,7 @@ Tensor kv_compact(const Tensor& k_pages, const Tensor& v_pages, const Tensor& pa
   const int32_t* acc = int32s("accepted", accepted);
   Tensor done = output("status", status, at::kInt, {c.rows}, dev);
   check(attn_kv_compact(&c, cu, acc, as_int("accepted", accepted.size(0)), cu_acc, done.mutable_data_ptr<int32_t>(),
-                        stream_of(stream, dev)),
+                        on),
         attn_kv_strerror);
   return done;
 }
@@ -305,6 +330,7 @@ void kv_free(const Tensor& page_table, const Tensor& seq_lens, const Tensor& ref
   const std::initializer_list<Named> all = {
       {"page_table", page_table}, {"seq_lens", seq_lens}, {"ref_counts", ref_counts}, {"rows", rows}};
   const int dev = common_device(all);
+  const OnStream on(stream, dev);
   attn_kv_cache c{};
   put_rows(&c, page_table, seq_lens);
   c.ref_counts = const_cast<int32_t*>(int32s("ref_counts", ref_counts));
@@ -313,7 +339,7 @@ void kv_free(const Tensor& page_table, const Tensor& seq_lens, const Tensor& ref
   c.Hkv = 1;  // heads and D are not used
   c.D = 64;
   const int32_t* list = int32s("rows", rows);
-  check(attn_kv_free(&c, list, as_int("rows", rows.size(0)), stream_of(stream, dev)), attn_kv_strerror);
+  check(attn_kv_free(&c, list, as_int("rows", rows.size(0)), on), attn_kv_strerror);
 }
 
 }  // namespace

@@ -14,6 +14,12 @@ namespace attn_host {
 
 inline bool aligned_to(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  if (!a || !b || na == 0 || nb == 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a), b0 = reinterpret_cast<uintptr_t>(b);
+  return a0 < b0 + nb && b0 < a0 + na;
+}
+
 // One (page, head, slot) tensor: no two elements in one place (each dimension steps past
 // everything the smaller ones span), rows of D on 16-byte boundaries.
 inline bool strides_ok(int64_t page, int64_t head, int64_t slot, const attn_kv_cache& c) {

@@ -13,6 +13,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "attn_kv.h"
@@ -144,6 +145,10 @@ __global__ void __launch_bounds__(kPlan) kv_append_plan_kernel(const attn_kv_cac
     if (len < 0 || c0 < 0 || c1 < c0 || c1 > n_tokens) return -1;
     const int64_t end = static_cast<int64_t>(len) + (c1 - c0);
     if (end > static_cast<int64_t>(c.max_pages) * c.page_size) return -1;
+    if (c1 > c0 && len % c.page_size != 0) {  // goes on in the last page: it has to be the row's own
+      const int page = c.page_table[static_cast<int64_t>(b) * c.max_pages + len / c.page_size];
+      if (page < 0 || page >= c.n_pages || c.ref_counts[page] != 1) return -1;
+    }
     return pages_of(static_cast<int>(end), c.page_size) - pages_of(len, c.page_size);
   });
   if (bad) return report(status, ATTN_KV_INVALID);
@@ -347,6 +352,10 @@ __global__ void __launch_bounds__(kCompact) kv_compact_kernel(const attn_kv_cach
       }
     }
   }
+  if (!bad && m < n && (ctx + m) % c.page_size != 0) {  // the page it ends inside of has to be its own
+    const int page = table[(ctx + m) / c.page_size];
+    bad = page < 0 || page >= c.n_pages || c.ref_counts[page] != 1;
+  }
   bad = __syncthreads_or(bad);
   if (tid == 0) status[b] = bad ? ATTN_KV_INVALID : 0;
   if (bad) return;
@@ -480,8 +489,24 @@ int attn_kv_append(const attn_kv_cache* cache, const void* k_new, const void* v_
     if (!attn_host::aligned_to(k_new, 16) || !attn_host::aligned_to(v_new, 16)) return ATTN_ERR_MISALIGNED;
     const int64_t strides[] = {k_stride_token, k_stride_head, v_stride_token, v_stride_head};
     for (int64_t s : strides)
-      if (s < 0 || s % 8 != 0) return ATTN_ERR_INVALID_ARG;
-    if (cache->k == cache->v && cache->n_pages > 0) return ATTN_ERR_INVALID_ARG;
+      if (s < 0 || s % 8 != 0 || s > (INT64_MAX / 8) / std::max(n_tokens, cache->Hkv)) return ATTN_ERR_INVALID_ARG;
+    if (cache->n_pages > 0) {
+      if (cache->k == cache->v) return ATTN_ERR_INVALID_ARG;
+      // the new tokens must not lie in the pool
+      const struct {
+        const void* at;
+        int64_t end;  // elements it spans
+      } from[] = {{k_new, (n_tokens - 1) * k_stride_token + (cache->Hkv - 1) * k_stride_head + cache->D},
+                  {v_new, (n_tokens - 1) * v_stride_token + (cache->Hkv - 1) * v_stride_head + cache->D}},
+        to[] = {{cache->k, (cache->n_pages - 1) * cache->k_stride_page + (cache->Hkv - 1) * cache->k_stride_head +
+                               (cache->page_size - 1) * cache->k_stride_slot + cache->D},
+                {cache->v, (cache->n_pages - 1) * cache->v_stride_page + (cache->Hkv - 1) * cache->v_stride_head +
+                               (cache->page_size - 1) * cache->v_stride_slot + cache->D}};
+      for (const auto& a : from)
+        for (const auto& b : to)
+          if (attn_host::overlap(a.at, static_cast<size_t>(a.end) * 2, b.at, static_cast<size_t>(b.end) * 2))
+            return ATTN_ERR_INVALID_ARG;
+    }
   }
   int sms = 0;
   st = device(&sms);

@@ -235,6 +235,10 @@ size_t attn_fwd_tile_order_entries(int B, int order_heads, int Sq, int Sk);
  * Sq * Sk.  A row with no visible key gets O = 0 and LSE = -inf; a window of at
  * least max(Sq, Sk) gives attn_fwd's result.
  *
+ * K and V entries outside every window of a work item are not used; as in attn_fwd a
+ * NaN in V may reach every row of a work item (256 rows, or the same 128 of two heads)
+ * that loads the key's tile, also rows that do not see the key.
+ *
  * causal is 1 or 2, window >= 1, sinks >= 0 (ATTN_ERR_INVALID_ARG otherwise);
  * other arguments, layouts and status codes as attn_fwd.  One kernel is enqueued
  * on `stream`; nothing is allocated.  The work order is heads fastest always

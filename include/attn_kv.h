@@ -69,8 +69,9 @@ typedef struct {
  * tokens; those in no row's range are ignored.  cu_tokens: int32 [rows + 1].
  * status: int32 [1], written: 0; the number of pages missing; or ATTN_KV_INVALID
  * (cu_tokens falls or leaves [0, n_tokens], a length is negative, a row would pass
- * max_pages).  Unless it is 0 nothing has changed.  A row's last page must not be
- * shared while it is partly filled (attn_kv_fork leaves none).
+ * max_pages, or would go on in a partly filled page that another row lists too: the
+ * calls here leave none).  Unless it is 0 nothing has changed.  k_new and v_new must
+ * not lie in the pool.
  */
 int attn_kv_append(const attn_kv_cache* cache, const void* k_new, const void* v_new, int64_t k_stride_token,
                    int64_t k_stride_head, int64_t v_stride_token, int64_t v_stride_head, int n_tokens,
@@ -97,7 +98,8 @@ int attn_kv_fork(const attn_kv_cache* cache, const int32_t* parents, const int32
  * dropped.  accepted holds n_accepted entries.
  * status: int32 [rows], written: 0, or ATTN_KV_INVALID for a row that is left as it
  * was: offsets that fall or leave their arrays, a list that is not ascending or out of range,
- * n_b over the row's length, or a page that tokens would move into and another row shares.
+ * n_b over the row's length, or a page that another row shares and that tokens would move
+ * into or the row would end inside of (fork it first: the child gets a copy).
  */
 int attn_kv_compact(const attn_kv_cache* cache, const int32_t* cu_tokens, const int32_t* accepted, int n_accepted,
                     const int32_t* cu_accepted, int32_t* status, cudaStream_t stream);

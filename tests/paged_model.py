@@ -28,7 +28,9 @@ class Model:
         k_new, v_new = bits(k_new), bits(v_new)
         n = np.diff(cu)
         room = self.table.shape[1] * self.P
-        if (n < 0).any() or cu[0] < 0 or cu[-1] > len(k_new) or (self.lens < 0).any() or (self.lens + n > room).any():
+        own = all(m <= 0 or a % self.P == 0 or self.ref[self.table[b, a // self.P]] == 1
+                  for b, (a, m) in enumerate(zip(self.lens, n)) if 0 <= a < room)
+        if not own or (n < 0).any() or cu[0] < 0 or cu[-1] > len(k_new) or (self.lens < 0).any() or (self.lens + n > room).any():
             return -1
         want = sum(self.pages(a + m) - self.pages(a) for a, m in zip(self.lens, n))
         if want > self.free_pages():
@@ -81,7 +83,9 @@ class Model:
                 continue
             acc = [int(x) for x in accepted[a0:a1]]
             place = lambda t: (self.table[b, t // self.P], t % self.P)  # noqa: E731
-            if any(not 0 <= x < n for x in acc) or any(y <= x for x, y in zip(acc, acc[1:])) or \
+            end = ctx + len(acc)
+            inside = len(acc) < n and end % self.P and self.ref[place(end)[0]] != 1  # ends in a shared page
+            if inside or any(not 0 <= x < n for x in acc) or any(y <= x for x, y in zip(acc, acc[1:])) or \
                     any(x != i and self.ref[place(ctx + i)[0]] != 1 for i, x in enumerate(acc)):
                 status[b] = -1
                 continue

@@ -144,11 +144,29 @@ def test_shared_pages_are_not_moved_into():
     model = Model(*cache)
     append(cache, model, np.array([40, 0, 0]))
     assert fork(cache, model, [0], [1]) == 0
-    # tokens 30 and 31 of row 0 lie in a page that row 1 lists too: moving 31 to 30 is refused, dropping is not
+    # tokens 30 and 31 of row 0 lie in a page that row 1 lists too: moving 31 to 30 is refused, and so is an end
+    # inside the page, where the next token would be written over row 1's
     assert compact(cache, model, np.array([10, 0, 0]), [[1], [], []]).tolist() == [-1, 0, 0]
     same(model, cache)
-    assert compact(cache, model, np.array([20, 20, 0]), [[], [0, 1], []]).tolist() == [0, 0, 0]
+    assert compact(cache, model, np.array([20, 20, 0]), [[], [0, 1], []]).tolist() == [-1, -1, 0]
     same(model, cache)
+    # at a page's end it is not: row 1 keeps 32 tokens and goes on in a page of its own
+    assert compact(cache, model, np.array([0, 8, 0]), [[], [], []]).tolist() == [0, 0, 0]
+    assert append(cache, model, np.array([1, 3, 0])) == 0
+    same(model, cache)
+
+
+@gpu
+def test_a_partly_filled_page_that_is_shared_is_not_written():
+    # a table made by hand: two rows end inside one page
+    cache = empty_cache(4, 1, 16, 64, 2, 2)
+    cache[2][:, 0], cache[3][:], cache[4][0] = 0, 5, 2
+    model = Model(*cache)
+    assert append(cache, model, np.array([1, 0])) == ops.KV_INVALID
+    same(model, cache)
+    cache[2][0, 0] = 9  # no such page
+    k, v = new_tokens(1, 1, 64, 1)
+    assert ops.kv_append(k, v, *cache, i32([0, 1, 1])).item() == ops.KV_INVALID
 
 
 @gpu
@@ -329,6 +347,8 @@ def test_pointers_and_counts_that_are_refused(lib):
     assert call_append(lib, fake(), n=-1) == inv and call_append(lib, fake(), stride=4) == inv
     assert call_append(lib, fake(), stride=-128) == inv
     assert call_append(lib, fake(v=0x1000000)) == inv  # K and V in one place
+    assert call_append(lib, fake(), k=0x1000800) == inv  # new tokens in the pool
+    assert call_append(lib, fake(), stride=2 ** 61) == inv
     assert lib.attn_kv_fork(fake(), 0x6000000, 0x6100000, 5, 0x5100000, None) == inv  # more children than rows
     assert lib.attn_kv_fork(fake(), None, 0x6100000, 1, 0x5100000, None) == null
     assert lib.attn_kv_fork(fake(), 0x6000000, 0x6100000, 1, None, None) == null

@@ -278,6 +278,40 @@ def test_the_same_twice_in_a_graph_and_on_another_stream():
 
 
 @gpu
+def test_on_a_stream_that_is_not_the_current_one():
+    # outputs and workspace are allocated by the call, on its stream: work that the current stream does meanwhile
+    # must not get their memory
+    b = Batch([3000] * 6, [1] * 6, 32, 8, 128, 64, seed=15)
+    want = b.run()
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        side.wait_stream(torch.cuda.current_stream())
+        got = ops.attn_fwd_tree(b.q, b.k, b.v, b.table, b.seq_lens, b.cu, stream=side)
+        noise = [torch.full((n,), 7, dtype=torch.uint8, device="cuda")
+                 for n in (ops.tree_workspace_size(128), b.q.numel() * 2, 6 * 32 * 4)]
+        side.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+        del noise
+
+
+@gpu
+def test_a_pool_without_pages_and_no_tokens():
+    b = Batch([20, 7], [1, 2], 4, 2, 64, 16, seed=16)
+    b.k, b.v = b.k[:0], b.v[:0]
+    o, lse = ops.attn_fwd_tree(b.q, b.k, b.v, b.table, b.seq_lens, b.cu)  # every page is past the pool
+    assert ops.paged_debug_status()[0] == ops.ATTN_ERR_INVALID_ARG
+    seen = torch.tensor([20.0, 6.0, 7.0], device="cuda")  # zeros for K: each key weighs the same
+    assert torch.all(o == 0) and torch.allclose(lse, seen.log()[:, None].expand(3, 4), atol=1e-3)
+    none = torch.zeros((0, 2), dtype=torch.int32, device="cuda")
+    o, lse = ops.attn_fwd_tree(b.q[:0], b.k, b.v, b.table, b.seq_lens, i32([0, 0, 0]), tree_mask=none)
+    assert o.shape == (0, 4, 64) and lse.shape == (0, 4)
+    with pytest.raises(ValueError):
+        ops.attn_fwd_tree(b.q, b.k, b.v, b.table, b.seq_lens, b.cu, tree_mask=none.new_zeros((3, 0)))
+    with pytest.raises(ops.AttnError):
+        ops.attn_fwd_tree(b.q, b.k, b.v, b.table, b.seq_lens, b.cu, scale=-1.0)
+
+
+@gpu
 def test_many_rows():
     rng = np.random.default_rng(11)
     n = rng.integers(0, 3, 700)
@@ -399,8 +433,8 @@ def call(lib, cache=None, **kw):
 
 @pytest.mark.parametrize("kw", [dict(Hq=7), dict(Hq=0), dict(Hq=258), dict(T=-1), dict(window=-1), dict(sinks=-1),
                                 dict(scale=0.0), dict(scale=float("inf")), dict(words=0), dict(mask=None),
-                                dict(q_token=4), dict(q_head=-64), dict(q_head=0), dict(n=1000), dict(o=0x4000000), dict(lse=0x5000000),
-                                dict(ws=0x1000000), dict(ws=0x4000000), dict(o=0x3000000 - 64), dict(o=0x7100000)],
+                                dict(q_token=4), dict(q_head=-64), dict(q_head=0), dict(n=1000), dict(o=0x4000000),
+                                dict(lse=0x5000000), dict(ws=0x1000000), dict(ws=0x4000000), dict(o=0x3000000 - 64), dict(o=0x7100000)],
                          ids=lambda k: "-".join(map(str, k.items())))
 def test_arguments_that_are_refused(lib, kw):
     assert call(lib, **kw) == ops.ATTN_ERR_INVALID_ARG

@@ -222,7 +222,8 @@ def test_invalid_arguments(kw):
 
 
 def test_pointers_and_workspace():
-    fwd = lambda q=Q, o=O: _lib.load().attn_fwd_window(q, K, V, o, L, 1, 4, 2, 64, 64, 128, 1, 8, 2, 0.1, None)  # noqa: E731
+    fwd = lambda q=Q, o=O: _lib.load().attn_fwd_window(q, K, V, o, L, 1, 4, 2, 64, 64, 128, 1, 8, 2, 0.1,  # noqa: E731
+                                                       None)
     assert fwd(q=0) == ops.ATTN_ERR_NULL_PTR
     assert fwd(o=O + 4) == ops.ATTN_ERR_MISALIGNED
     assert fwd(o=K) == ops.ATTN_ERR_INVALID_ARG
