@@ -23,7 +23,7 @@
 //   warp  11    TMA of the Q rows
 // Pairs (PAIR).  With more tokens than a row tile holds an item is two row tiles that share
 // each K and V tile: warps 0-3 and 4-7 take one each and convert half of V each.  Eight
-// trees of 32 to 64 tokens, 4 heads per kv head, up to 16384 keys, D 128: 130 us, against
+// trees of 32 to 64 tokens, 4 heads per kv head, up to 16384 keys, D 128: 127 us, against
 // 152 with the row tiles apart, which read K and V twice.
 // Key groups.  A thread of a softmax warp sees one TMEM lane, one row; with 32 rows or
 // fewer (a token or a few per sequence) three of the four warps would idle while one takes
@@ -94,8 +94,9 @@ struct Cfg {
   static constexpr int kTileBytes = BN * D * 2;
   static constexpr int kColBlockBytes = BN * 128;
   static constexpr int kQ = PAIR ? 2 : 1;  // row tiles of an item
-  // slots of the K and of the V ring: with Q some 224 KB in all
-  static constexpr int kK = D == 128 ? 3 : 6;
+  // slots of the K and of the V ring: with Q some 224 KB in all.  A V slot is held longer than a K slot (S
+  // runs ahead of PV), so where there is an odd one it is V's (pair, D 128: 127 us instead of 130).
+  static constexpr int kK = D == 128 ? (PAIR ? 2 : 3) : (PAIR ? 5 : 6);
   static constexpr int kV = (D == 128 ? 7 : 14) - kQ - kK;
   static constexpr int kSmemBytes = (kQ + kK + kV) * kTileBytes + 1024;
   // registers per thread of the three warpgroups
@@ -1434,7 +1435,7 @@ int attn_fwd_tree(const attn_kv_cache* cache, const void* q, int64_t q_stride_to
   p.G = Hq / c.Hkv;
   p.R = BM / p.G;
   // Pairs of row tiles, which share each key tile, when the sequences have more tokens than a row tile
-  // on average (130 us instead of 152, see the head).  With fewer the second softmax warps would only
+  // on average (127 us instead of 152, see the head).  With fewer the second softmax warps would only
   // convert, and V has a slot less: one token each, 272 us instead of 240 (D 128), 135 instead of 109 (D 64).
   p.item_tokens = n_tokens > static_cast<int64_t>(p.R) * c.rows ? 2 * p.R : p.R;
   p.G_inv = (65536u + p.G - 1) / p.G;
