@@ -1074,19 +1074,25 @@ int64_t padded_rows(int Sq) { return (static_cast<int64_t>(Sq) + BT - 1) / BT * 
 
 // Window mode: how the dK/dV work of the key tiles that hold sinks is cut.  Such a tile is
 // seen by every later query tile, a tile without sinks by about window / 128 + 2 of them;
-// chunks of that many query tiles (eight at least) make the items about equal.
+// chunks of that many query tiles (eight at least) make the items about equal.  With many sinks
+// the chunks are longer, so that there are at most kMaxSinkItems (7 per SM) and the partials
+// take 134 MB at most (32768 tokens, 32 / 8 heads, window 1024, 4096 sinks: 6.26 ms, 6.76 with
+// 840 MB of chunks as short as for a few sinks; every key a sink: 19.8 ms, 23.9 with 6.7 GB).
 struct SinkPlan {
   int tiles, chunks, per;
   size_t bytes;  // of the fp32 partials
 };
 
 constexpr int kMaxSinkChunks = 64;
+constexpr int kMaxSinkItems = 1024;
 
 SinkPlan sink_plan(int64_t BZ, int Sq, int Sk, int D, int window, int sinks) {
   SinkPlan s;
   s.tiles = (std::min(sinks, Sk) + BT - 1) / BT;
   const int n_qt = static_cast<int>(padded_rows(Sq) / BT);
-  s.per = std::max({window / BT + 2, 8, (n_qt + kMaxSinkChunks - 1) / kMaxSinkChunks});
+  const int most = static_cast<int>(
+      std::clamp<int64_t>(kMaxSinkItems / std::max<int64_t>(s.tiles * BZ, 1), 1, kMaxSinkChunks));
+  s.per = std::max({window / BT + 2, 8, (n_qt + most - 1) / most});
   s.chunks = s.tiles > 0 ? std::max((n_qt + s.per - 1) / s.per, 1) : 1;
   s.bytes = s.chunks > 1 ? static_cast<size_t>(s.tiles) * s.chunks * BZ * 2 * BT * D * 4 : 0;
   return s;

@@ -1439,7 +1439,7 @@ int attn_fwd_tree(const attn_kv_cache* cache, const void* q, int64_t q_stride_to
   // convert, and V has a slot less: one token each, 272 us instead of 240 (D 128), 135 instead of 109 (D 64).
   p.item_tokens = n_tokens > static_cast<int64_t>(p.R) * c.rows ? 2 * p.R : p.R;
   p.G_inv = (65536u + p.G - 1) / p.G;
-  p.window = std::min(window, 1 << 30);  // no key is further away (rows hold less than 2^31 tokens)
+  p.window = std::min(window, 1 << 30);  // no key is further away
   p.sinks = std::min(sinks, 1 << 30);
   p.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
   p.part_o = reinterpret_cast<float*>(ws + w.o);

@@ -163,10 +163,9 @@ __global__ void __launch_bounds__(kPlan) kv_append_plan_kernel(const attn_kv_cac
   report(status, missing);
 }
 
-// The row that token t belongs to (cu[b] <= t < cu[b + 1]), or -1; the warp's lanes probe 32
-// offsets at a time, so 1024 rows take two loads.
+// The row that token t belongs to (cu[b] <= t < cu[b + 1]); the warp's lanes probe 32 offsets at
+// a time, so 1024 rows take two loads.
 __device__ __forceinline__ int row_of(const int32_t* cu, int rows, int t) {
-  if (t < cu[0] || t >= cu[rows]) return -1;
   const int lane = static_cast<int>(threadIdx.x % 32);
   int lo = 0, n = rows;
   while (n > 1) {
@@ -183,7 +182,6 @@ __device__ __forceinline__ int row_of(const int32_t* cu, int rows, int t) {
 struct NewTokens {
   const __nv_bfloat16 *k, *v;
   int64_t k_token, k_head, v_token, v_head;
-  int n;
 };
 
 // One warp per token: its K and V of every head, 16 bytes per lane and access, four of each in flight.
@@ -197,9 +195,10 @@ __global__ void __launch_bounds__(256) kv_append_write_kernel(const attn_kv_cach
   if (*status != 0) return;
   const int lane = threadIdx.x % 32;
   const int per = c.Hkv * kChunks;
-  for (int t = (blockIdx.x * 256 + threadIdx.x) / 32; t < x.n; t += gridDim.x * 8) {
+  const int64_t last = cu[c.rows];
+  for (int64_t at = cu[0] + static_cast<int64_t>(blockIdx.x * 8 + threadIdx.x / 32); at < last; at += gridDim.x * 8) {
+    const int t = static_cast<int>(at);
     const int b = row_of(cu, c.rows, t);
-    if (b < 0) continue;
     const int pos = c.seq_lens[b] - (cu[b + 1] - t);
     const int page = c.page_table[static_cast<int64_t>(b) * c.max_pages + pos / c.page_size];
     if (page < 0 || page >= c.n_pages) continue;
@@ -259,7 +258,9 @@ __global__ void __launch_bounds__(kPlan) kv_fork_plan_kernel(const attn_kv_cache
     if (a < 0 || a >= c.rows || ((is_child[a / 32] >> (a % 32)) & 1u)) return -1;
     const int len = c.seq_lens[a];
     if (len < 0 || len > static_cast<int64_t>(c.max_pages) * c.page_size) return -1;
-    return len % c.page_size != 0 ? 1 : 0;
+    if (len % c.page_size == 0) return 0;
+    const int page = c.page_table[static_cast<int64_t>(a) * c.max_pages + len / c.page_size];
+    return page < 0 || page >= c.n_pages ? -1 : 1;  // the page to copy
   });
   if (bad) return report(status, ATTN_KV_INVALID);
   const int missing = hand_out(c, want, [&](uint32_t k, int page) {
@@ -302,7 +303,6 @@ __global__ void __launch_bounds__(256) kv_fork_move_kernel(const attn_kv_cache c
   }
   if (part == 0) return;
   const int src = from[full], dst = to[full];
-  if (src < 0 || src >= c.n_pages || dst < 0 || dst >= c.n_pages) return;
   const int h = blockIdx.y - 1;
   const __nv_bfloat16* k = static_cast<const __nv_bfloat16*>(c.k) + h * c.k_stride_head;
   const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(c.v) + h * c.v_stride_head;
@@ -319,9 +319,11 @@ __global__ void __launch_bounds__(256) kv_fork_move_kernel(const attn_kv_cache c
 }
 
 // ---------------------------------------------------------------------------- compact
-// One block per row.  Token i of the kept ones comes from place accepted[i] >= i, so
-// moving them in ascending order never overwrites a token that is still to move; a group
-// of tokens is read whole into registers before any of it is written.
+// One block per row checks its lists and moves its tokens, then a second kernel gives pages
+// back and sets the lengths: a page counts as shared if it was before the call, whichever
+// block runs first.  Token i of the kept ones comes from place accepted[i] >= i, so moving them
+// in ascending order never overwrites a token that is still to move; a group of tokens is
+// read whole into registers before any of it is written.
 constexpr int kCompact = 512;  // threads
 constexpr int kHold = 4;       // 16-byte pieces of K and of V that a thread holds
 constexpr int kGroup = 128;    // tokens whose places are looked up at a time
@@ -333,11 +335,12 @@ __global__ void __launch_bounds__(kCompact) kv_compact_kernel(const attn_kv_cach
                                                               int32_t* __restrict__ status) {
   constexpr int kChunks = D / 8;
   __shared__ int2 s_from[kGroup], s_to[kGroup];  // page, slot
+  griddep_launch_dependents();
   const int b = blockIdx.x, tid = threadIdx.x;
   const int len = c.seq_lens[b];
   const int n = cu[b + 1] - cu[b];
   const int a0 = cu_accepted[b], a1 = cu_accepted[b + 1];
-  int32_t* table = c.page_table + static_cast<int64_t>(b) * c.max_pages;
+  const int32_t* table = c.page_table + static_cast<int64_t>(b) * c.max_pages;
   const int ctx = len - n, m = a1 - a0;
   // ---- the row's lists
   bool bad = n < 0 || ctx < 0 || len > static_cast<int64_t>(c.max_pages) * c.page_size || a0 < 0 || m < 0 ||
@@ -401,14 +404,25 @@ __global__ void __launch_bounds__(kCompact) kv_compact_kernel(const attn_kv_cach
       __syncthreads();  // ... and written before the next one is read
     }
   }
-  // ---- the new length; pages past it
-  __syncthreads();
-  for (int p = pages_of(ctx + m, c.page_size) + tid; p < pages_of(len, c.page_size); p += kCompact) {
+}
+
+// The lengths after kv_compact_kernel, and the pages past them, a warp per row.
+__global__ void __launch_bounds__(256) kv_compact_end_kernel(const attn_kv_cache c, const int32_t* __restrict__ cu,
+                                                             const int32_t* __restrict__ cu_accepted,
+                                                             const int32_t* status) {
+  const int b = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
+  griddep_wait();
+  if (b >= c.rows || status[b] != 0) return;
+  const int len = c.seq_lens[b];
+  const int end = len - (cu[b + 1] - cu[b]) + (cu_accepted[b + 1] - cu_accepted[b]);
+  int32_t* table = c.page_table + static_cast<int64_t>(b) * c.max_pages;
+  for (int p = pages_of(end, c.page_size) + lane; p < pages_of(len, c.page_size); p += 32) {
     const int page = table[p];
     if (page >= 0 && page < c.n_pages) atomicSub(&c.ref_counts[page], 1);
     table[p] = -1;
   }
-  if (tid == 0) c.seq_lens[b] = ctx + m;
+  __syncwarp();
+  if (lane == 0) c.seq_lens[b] = end;
 }
 
 // ---------------------------------------------------------------------------- free
@@ -487,6 +501,9 @@ int attn_kv_append(const attn_kv_cache* cache, const void* k_new, const void* v_
   if (n_tokens > 0) {
     if (!k_new || !v_new) return ATTN_ERR_NULL_PTR;
     if (!attn_host::aligned_to(k_new, 16) || !attn_host::aligned_to(v_new, 16)) return ATTN_ERR_MISALIGNED;
+    // the stride of a dimension of one element is not used
+    if (n_tokens == 1) k_stride_token = v_stride_token = 0;
+    if (cache->Hkv == 1) k_stride_head = v_stride_head = 0;
     const int64_t strides[] = {k_stride_token, k_stride_head, v_stride_token, v_stride_head};
     for (int64_t s : strides)
       if (s < 0 || s % 8 != 0 || s > (INT64_MAX / 8) / std::max(n_tokens, cache->Hkv)) return ATTN_ERR_INVALID_ARG;
@@ -519,8 +536,8 @@ int attn_kv_append(const attn_kv_cache* cache, const void* k_new, const void* v_
   if (e != cudaSuccess) return cuda_fail(e);
   if (n_tokens == 0 || cache->rows == 0 || cache->n_pages == 0) return ATTN_OK;
   const NewTokens x{static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new),
-                    k_stride_token, k_stride_head, v_stride_token, v_stride_head, n_tokens};
-  const int blocks = std::min((n_tokens + 7) / 8, sms * 8);
+                    k_stride_token, k_stride_head, v_stride_token, v_stride_head};
+  const int blocks = std::min(n_tokens / 8 + 1, sms * 8);
   return done(cache->D == 128
                   ? launch_after(kv_append_write_kernel<128>, dim3(blocks), 256, stream, *cache, x, cu_tokens, status)
                   : launch_after(kv_append_write_kernel<64>, dim3(blocks), 256, stream, *cache, x, cu_tokens, status));
@@ -570,7 +587,10 @@ int attn_kv_compact(const attn_kv_cache* cache, const int32_t* cu_tokens, const 
   else
     kv_compact_kernel<64><<<cache->rows, kCompact, 0, stream>>>(*cache, cu_tokens, accepted, n_accepted, cu_accepted,
                                                                 status);
-  return done(cudaGetLastError());
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e);
+  return done(launch_after(kv_compact_end_kernel, dim3((cache->rows + 7) / 8), 256, stream, *cache, cu_tokens,
+                           cu_accepted, status));
 }
 
 int attn_kv_free(const attn_kv_cache* cache, const int32_t* rows, int n, cudaStream_t stream) {

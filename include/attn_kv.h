@@ -18,7 +18,8 @@
  *     seq_lens    int32 [rows]: tokens of each row, the newest (drafted) ones included
  *     ref_counts  int32 [n_pages]: rows that list the page; 0 is a free page
  * D is 64 or 128; page_size 16, 32, 64, 128 or 256; rows at most 32768; n_pages at most
- * 4000000; k, v 16-byte aligned, the int32 arrays 4-byte aligned.
+ * 4000000; max_pages * page_size at most 2^30; k, v 16-byte aligned, the int32 arrays
+ * 4-byte aligned.
  *
  * A call that takes pages takes the free pages with the lowest numbers, in the order
  * of the rows (or pairs) and of their tokens, so equal states and calls give equal
@@ -45,6 +46,7 @@ extern "C" {
 
 #define ATTN_KV_MAX_ROWS 32768
 #define ATTN_KV_MAX_PAGES 4000000
+#define ATTN_KV_MAX_TOKENS (1 << 30) /* places of a row: its tiles' bounds stay within 32 bits */
 
 /* Device status words: 0 done, a positive number the pages that were missing, or */
 #define ATTN_KV_INVALID (-1) /* lengths, indices or lists that do not fit each other */
@@ -84,7 +86,7 @@ int attn_kv_append(const attn_kv_cache* cache, const void* k_new, const void* v_
  * have several children.  The child's table entries past its pages become -1.
  * status: int32 [1], written: 0; the number of pages missing; or ATTN_KV_INVALID (an
  * index out of range, a child that is not empty, is listed twice or is a parent
- * too).  Unless it is 0 nothing has changed.
+ * too, a partly filled page that is not in the pool).  Unless it is 0 nothing has changed.
  */
 int attn_kv_fork(const attn_kv_cache* cache, const int32_t* parents, const int32_t* children, int n, int32_t* status,
                  cudaStream_t stream);
@@ -98,8 +100,9 @@ int attn_kv_fork(const attn_kv_cache* cache, const int32_t* parents, const int32
  * dropped.  accepted holds n_accepted entries.
  * status: int32 [rows], written: 0, or ATTN_KV_INVALID for a row that is left as it
  * was: offsets that fall or leave their arrays, a list that is not ascending or out of range,
- * n_b over the row's length, or a page that another row shares and that tokens would move
- * into or the row would end inside of (fork it first: the child gets a copy).
+ * n_b over the row's length, or a page that another row listed before the call and that
+ * tokens would move into or the row would end inside of (fork it first: the child gets
+ * a copy).
  */
 int attn_kv_compact(const attn_kv_cache* cache, const int32_t* cu_tokens, const int32_t* accepted, int n_accepted,
                     const int32_t* cu_accepted, int32_t* status, cudaStream_t stream);

@@ -48,7 +48,8 @@ class Model:
         rows = len(self.lens)
         ok = all(0 <= x < rows for x in (*parents, *children)) and len(set(children)) == len(children) and \
             not set(parents) & set(children) and all(self.lens[c] == 0 for c in children) and \
-            all(0 <= self.lens[a] <= self.table.shape[1] * self.P for a in parents)
+            all(0 <= self.lens[a] <= self.table.shape[1] * self.P for a in parents) and \
+            all(0 <= self.table[a, self.lens[a] // self.P] < len(self.ref) for a in parents if self.lens[a] % self.P)
         if not ok:
             return -1
         want = sum(int(self.lens[a] % self.P != 0) for a in parents)
@@ -74,7 +75,7 @@ class Model:
         self.lens[b] = keep
 
     def compact(self, cu, accepted, cu_acc):
-        status = np.zeros(len(self.lens), np.int32)
+        status, ref = np.zeros(len(self.lens), np.int32), self.ref.copy()
         for b in range(len(self.lens)):
             n, a0, a1 = int(cu[b + 1] - cu[b]), int(cu_acc[b]), int(cu_acc[b + 1])
             ctx = int(self.lens[b]) - n
@@ -84,9 +85,9 @@ class Model:
             acc = [int(x) for x in accepted[a0:a1]]
             place = lambda t: (self.table[b, t // self.P], t % self.P)  # noqa: E731
             end = ctx + len(acc)
-            inside = len(acc) < n and end % self.P and self.ref[place(end)[0]] != 1  # ends in a shared page
+            inside = len(acc) < n and end % self.P and ref[place(end)[0]] != 1  # ends in a shared page
             if inside or any(not 0 <= x < n for x in acc) or any(y <= x for x, y in zip(acc, acc[1:])) or \
-                    any(x != i and self.ref[place(ctx + i)[0]] != 1 for i, x in enumerate(acc)):
+                    any(x != i and ref[place(ctx + i)[0]] != 1 for i, x in enumerate(acc)):
                 status[b] = -1
                 continue
             for i, x in enumerate(acc):

@@ -170,6 +170,55 @@ def test_a_partly_filled_page_that_is_shared_is_not_written():
 
 
 @gpu
+def test_a_page_counts_as_shared_if_it_was_before_the_call():
+    # of two rows that list one full page, one drops it and the other would end inside of it: refused whichever
+    # block runs first, so 40 such pairs all give the same
+    pairs = 40
+    cache = empty_cache(3 * pairs, 1, 16, 64, 2 * pairs, 2)
+    model = Model(*cache)
+    append(cache, model, np.repeat([16, 0], pairs))
+    fork(cache, model, np.arange(pairs), np.arange(pairs, 2 * pairs))
+    first = np.arange(pairs) % 2 == 0  # the parent drops the page and the child cuts into it, or the reverse
+    n = np.concatenate([np.where(first, 16, 5), np.where(first, 5, 16)])
+    assert compact(cache, model, n, [[]] * (2 * pairs)).tolist() == np.where(n == 5, -1, 0).tolist()
+    same(model, cache)
+
+
+@gpu
+def test_a_fork_of_a_page_that_is_not_there():
+    cache = empty_cache(4, 1, 16, 64, 2, 2)
+    model = Model(*cache)
+    append(cache, model, np.array([5, 0]))
+    for page in (-1, 4):
+        cache[2][0, 0] = page
+        assert ops.kv_fork(*cache, i32([0]), i32([1])).item() == ops.KV_INVALID
+        assert cache[2][1].tolist() == [-1, -1] and cache[3].tolist() == [5, 0] and cache[4].tolist() == [1, 0, 0, 0]
+
+
+@gpu
+def test_broadcast_tokens_and_as_many_as_32_bits_count():
+    # every token the same (stride 0): 2^31 - 1 of them, of which the rows take five
+    cache = empty_cache(4, 2, 16, 64, 2, 2)
+    model = Model(*cache)
+    k, v = new_tokens(1, 2, 64, 4)
+    many = [t.expand(2 ** 31 - 1, 2, 64) for t in (k, v)]
+    for lo in (0, 2 ** 31 - 6):
+        assert ops.kv_append(*many, *cache, i32([lo, lo + 2, lo + 5])).item() == 0
+        model.append(k.expand(5, 2, 64), v.expand(5, 2, 64), np.array([0, 2, 5]))
+        same(model, cache)
+
+
+@gpu
+def test_the_stride_of_one_element_is_not_used():
+    cache = empty_cache(2, 1, 16, 64, 1, 1)
+    model = Model(*cache)
+    k, v = (t.as_strided((1, 1, 64), (3, 5, 1)) for t in new_tokens(1, 1, 64, 4))
+    assert ops.kv_append(k, v, *cache, i32([0, 1])).item() == 0
+    model.append(k, v, np.array([0, 1]))
+    same(model, cache)
+
+
+@gpu
 def test_freeing_twice_and_out_of_range():
     cache = empty_cache(8, 1, 16, 64, 3, 2)
     model = Model(*cache)
@@ -321,7 +370,7 @@ def call_append(lib, cache, k=0x4000000, n=4, cu=0x5000000, status=0x5100000, st
 
 BAD_CACHES = [
     dict(D=96), dict(page_size=8), dict(page_size=48), dict(page_size=512), dict(Hkv=0), dict(rows=-1),
-    dict(rows=32769), dict(n_pages=4000001), dict(n_pages=-1), dict(max_pages=-1), dict(max_pages=2 ** 28),
+    dict(rows=32769), dict(n_pages=4000001), dict(n_pages=-1), dict(max_pages=-1), dict(max_pages=2 ** 28), dict(max_pages=2 ** 26 + 1),
     dict(k_stride_slot=0), dict(k_stride_slot=60), dict(k_stride_head=0), dict(v_stride_page=1024),
     dict(v_stride_page=-4096), dict(k_stride_page=2 ** 61),
 ]

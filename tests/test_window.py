@@ -111,6 +111,17 @@ def test_a_window_over_everything_is_the_dense_call_bitwise(D):
 
 
 @pytest.mark.gpu
+def test_so_many_sinks_that_their_tiles_are_not_cut_are_the_dense_call_bitwise():
+    # 33 tiles with sinks in each of 64 kv slices: one item each, whose query tiles come in the dense call's order
+    q, k, v = [t.cuda() for t in draw(32, 2, 2, 4224, 4224, 64, seed=25)]
+    do = draw(32, 2, 2, 4224, 4224, 64, seed=26)[0].cuda()
+    o, lse = ops.attn_fwd(q, k, v, causal=1)
+    a = ops.attn_bwd(q, k, v, o, lse, do, causal=1)
+    b = ops.attn_bwd_window(q, k, v, o, lse, do, 1, sinks=4224)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.gpu
 def test_keys_out_of_every_window_do_not_matter():
     # K rows that no row sees hold infinities and NaN, in tiles that are loaded for their other keys
     q, k, v = draw(1, 2, 1, 100, 1000, 128, seed=31)
@@ -237,6 +248,10 @@ def test_pointers_and_workspace():
     assert bwd(n=need - 1) == ops.ATTN_ERR_INVALID_ARG
     assert bwd(ws=0) == ops.ATTN_ERR_NULL_PTR
     assert bwd(ws=0x7000000) == ops.ATTN_ERR_INVALID_ARG  # over dq
+    # many sinks: at most 1024 partials of dV and dK
+    for sinks in (1024, 4096, 32768, 2 ** 31 - 1):
+        size = ops.bwd_window_workspace_size(1, 32, 8, 32768, 32768, 128, 1024, sinks)
+        assert 0 <= size - 2 * 32 * 32768 * 4 <= 1024 * 2 * 128 * 128 * 4
     for bad in (dict(window=0), dict(sinks=-1), dict(D=96), dict(Hkv=0)):
         a = dict(dict(B=1, Hq=4, Hkv=2, Sq=64, Sk=64, D=128, window=8, sinks=2), **bad)
         assert lib.attn_bwd_window_workspace_size(*a.values()) == 0
