@@ -9,6 +9,13 @@
 // its place in the order of requests, a second one over the reference counts numbers the free
 // pages, and free page k goes to the row whose requests cover k (binary search).
 // There is no list of free pages to keep in step: a count of 0 is a free page.
+//
+// Measured (graph of 20 calls; 8 kv heads, D 128, pages of 64): appending 1 / 64 / 512 tokens 6.4 /
+// 8.3 / 8.0 us, four forks that copy half a page each 8.6 us, keeping 4 of 8 tokens of 64 rows 4.8 us:
+// the latency of two kernels and their dependent loads.  16 prompts of 4096 to 8192 tokens: the
+// writing kernel takes 122 us for 805 MB, 6.6 TB/s.  Planning and moving in one launch of a cluster of
+// eight blocks, which saves the host 3 us, takes as long up to 8 tokens and 2 to 11 us longer from
+// 32 to 1024, since eight SMs move the rows.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -78,6 +85,26 @@ __device__ __forceinline__ uint64_t sum_requests(int count, uint32_t* off, bool&
   return carry;
 }
 
+// Which of the pages [p0, p0 + kScan) are free, as bits.
+__device__ __forceinline__ uint32_t free_bits(const int32_t* ref, int n_pages, int p0) {
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < kScan; ++i)
+    if (p0 + i < n_pages && ref[p0 + i] == 0) bits |= 1u << i;
+  return bits;
+}
+
+// put(k, page), put(k + 1, page), .. for the pages of `bits`, up to the `want`-th.
+template <class Put>
+__device__ __forceinline__ void give(uint32_t bits, int p0, uint32_t k, uint64_t want, Put put) {
+#pragma unroll
+  for (int i = 0; i < kScan; ++i)
+    if ((bits >> i) & 1u) {
+      if (k < want) put(k, p0 + i);
+      ++k;
+    }
+}
+
 // Walks the free pages in ascending order until `want` of them have been seen; put(k, page)
 // for the k-th (k < want).  Returns how many were found.
 template <class Put>
@@ -85,18 +112,10 @@ __device__ __forceinline__ uint32_t walk_free(const int32_t* ref, int n_pages, u
   uint32_t found = 0;
   for (int base = 0; base < n_pages && found < want; base += kPlan * kScan) {
     const int p0 = base + static_cast<int>(threadIdx.x) * kScan;
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < kScan; ++i)
-      if (p0 + i < n_pages && ref[p0 + i] == 0) bits |= 1u << i;
+    const uint32_t bits = free_bits(ref, n_pages, p0);
     uint32_t total;
-    uint32_t k = found + block_scan(static_cast<uint32_t>(__popc(bits)), total);
-#pragma unroll
-    for (int i = 0; i < kScan; ++i)
-      if ((bits >> i) & 1u) {
-        if (k < want) put(k, p0 + i);
-        ++k;
-      }
+    const uint32_t k = found + block_scan(static_cast<uint32_t>(__popc(bits)), total);
+    give(bits, p0, k, want, put);
     found += total;
   }
   return found;
@@ -120,6 +139,19 @@ __device__ __forceinline__ int taker_of(const uint32_t* off, int count, uint32_t
 template <class Put>
 __device__ __forceinline__ int hand_out(const attn_kv_cache& c, uint64_t want, Put put) {
   if (want == 0) return 0;
+  // one step of the walk: each thread keeps what it read (0.6 us less than walking twice)
+  if (c.n_pages <= kPlan * kScan) {
+    const int p0 = static_cast<int>(threadIdx.x) * kScan;
+    const uint32_t bits = free_bits(c.ref_counts, c.n_pages, p0);
+    uint32_t found;
+    const uint32_t k = block_scan(static_cast<uint32_t>(__popc(bits)), found);
+    if (found < want) return static_cast<int>(min(want - found, static_cast<uint64_t>(INT32_MAX)));
+    give(bits, p0, k, want, [&](uint32_t i, int page) {
+      put(i, page);
+      c.ref_counts[page] = 1;
+    });
+    return 0;
+  }
   const uint64_t found = walk_free(c.ref_counts, c.n_pages, want, [](uint32_t, int) {});
   if (found < want) return static_cast<int>(min(want - found, static_cast<uint64_t>(INT32_MAX)));
   // a page is given away by the thread that reads its count, so the walk sees each once
