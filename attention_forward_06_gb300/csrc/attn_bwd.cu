@@ -87,14 +87,15 @@ struct BParams {
   float scale;
   // window mode: key j also needs row + diag - j < window or j < sinks.  A key tile that
   // holds sinks is seen by every later query tile; its dK/dV work is cut into sink_chunks
-  // items of sink_per query tiles, which leave fp32 partials (sink_chunks > 1) for
-  // attn_bwd_sink_kernel
+  // items of sink_per query tiles.  Where there are few items they are cut by heads too.  A
+  // tile that is cut has fp32 partials, which attn_bwd_parts_kernel adds
   int window;       // 1 .. max(Sq, Sk)
   int sinks;        // 0 .. Sk
-  int sink_tiles;   // key tiles that hold sinks
   int sink_chunks;  // items per such tile and kv slice
   int sink_per;     // query tiles per chunk
-  float* sink_part; // [sink_tiles][sink_chunks][B*Hkv][dV, dK][BT][D]
+  int head_groups;  // items that such a chunk's, or another tile's, query heads are cut into
+  __host__ __device__ int sink_tiles() const { return (sinks + BT - 1) / BT; }  // key tiles that hold sinks
+  float* part;      // [item / (B*Hkv)][B*Hkv][dV, dK][BT][D], the items of tiles that are cut
 };
 
 __device__ int g_bwd_status;
@@ -252,29 +253,38 @@ __device__ __forceinline__ int first_qtile(const BParams& p, int j) {
   return first_row / BT;
 }
 
-// A dK/dV work item: key tile j of kv slice z against query tiles [i0, i0 + nI) of every
-// query head of the group.
+// A dK/dV work item: key tile j of kv slice z against query tiles [i0, i0 + nI) of the heads
+// [h0, h0 + nH) of its group.
 struct KvItem {
   int j, z, i0, nI;
+  int h0, nH;  // cut by heads (otherwise the whole group)
   int part;  // window mode: the slot of the fp32 partial it writes (-1: it writes dK and dV)
 };
 
-template <bool WINDOW>
+template <bool WINDOW, bool CUT>
 __device__ __forceinline__ KvItem kv_item(const BParams& p, int x) {
   KvItem it;
   it.part = -1;
   if constexpr (WINDOW) {
-    // the chunks of the tiles that hold sinks come first, then the other tiles in order
-    const int n_chunked = p.sink_tiles * p.sink_chunks;
-    const int y = x / p.BZ;
+    // the chunks of the tiles that hold sinks come first, then the other tiles in order; the
+    // head groups of each are next to one another
+    const int n_chunked = p.sink_tiles() * p.sink_chunks;
+    int y = x / p.BZ;
     it.z = x % p.BZ;
+    if constexpr (CUT) {
+      const int heads = (p.G + p.head_groups - 1) / p.head_groups;
+      it.h0 = y % p.head_groups * heads;
+      it.nH = min(p.G - it.h0, heads);
+      it.part = x;
+      y /= p.head_groups;
+    }
     if (y < n_chunked) {
       it.j = y / p.sink_chunks;
       it.i0 = first_qtile(p, it.j) + (y % p.sink_chunks) * p.sink_per;
       it.nI = min(p.n_qt - it.i0, p.sink_per);
-      if (p.sink_chunks > 1) it.part = x;
+      if (!CUT && p.sink_chunks > 1) it.part = x;
     } else {
-      it.j = y - n_chunked + p.sink_tiles;
+      it.j = y - n_chunked + p.sink_tiles();
       it.i0 = first_qtile(p, it.j);
       // the last row that has a key of the tile in its window
       const int last = min(p.Sq, min(it.j * BT + BT, p.Sk) + p.window - 1 - p.diag) - 1;
@@ -300,8 +310,9 @@ __device__ __forceinline__ KvItem kv_item(const BParams& p, int x) {
 // exponentials run while the tensor cores work on the other half:
 //   S_0(s) S_1(s) | dVdK_0(s) S_0(s+1) dVdK_1(s) S_1(s+1) | ...
 // Window mode: the items of kv_item; a key tile without sinks meets only the query
-// tiles whose windows reach it.
-template <int D, bool WINDOW = false>
+// tiles whose windows reach it.  CUT: an item is some of the group's heads (its own kernel, as the
+// others would be 1 % slower with the heads read from the item).
+template <int D, bool WINDOW = false, bool CUT = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                          const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -360,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k * static_cast<int>(gridDim.x) < p.n_items && ok; ++k) {
       const int x = item_of(k);
       if (x >= p.n_items) continue;
-      const KvItem item = kv_item<WINDOW>(p, x);
+      const KvItem item = kv_item<WINDOW, CUT>(p, x);
       const int j = item.j, z = item.z, i0 = item.i0, nI = item.nI;
       if (nI <= 0) continue;
       if (n_ne > 0) ok = warp_wait(&kv_empty, (n_ne - 1) & 1, abort_v, kTimeoutNs);
@@ -374,8 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++n_ne;
       const int b = z / p.Hkv, kvh = z % p.Hkv;
-      for (int s = 0; s < G * nI && ok; ++s, ++it) {
-        const int h = kvh * G + s / nI, i = i0 + s % nI;
+      for (int s = 0; s < (CUT ? item.nH : G) * nI && ok; ++s, ++it) {
+        const int h = kvh * G + (CUT ? item.h0 : 0) + s / nI, i = i0 + s % nI;
         const int bh = b * p.Hq + h;
         const uint32_t slot = it % kRing, use = it / kRing;
         if (use > 0) ok = warp_wait(&empty[slot], (use - 1) & 1, abort_v, kTimeoutNs);
@@ -433,9 +444,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k * static_cast<int>(gridDim.x) < p.n_items && ok; ++k) {
       const int x = item_of(k);
       if (x >= p.n_items) continue;
-      const int nI = kv_item<WINDOW>(p, x).nI;
-      if (nI <= 0) continue;
-      const int T = G * nI;  // steps of the item
+      const KvItem item = kv_item<WINDOW, CUT>(p, x);
+      if (item.nI <= 0) continue;
+      const int T = (CUT ? item.nH : G) * item.nI;  // steps of the item
       ok = warp_wait(&kv_full, n_ne & 1, abort_v, kTimeoutNs);
       if (ok) ok = warp_wait(&full[it % kRing], (it / kRing) & 1, abort_v, kTimeoutNs);
       if (!ok) break;
@@ -496,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k * static_cast<int>(gridDim.x) < p.n_items && ok; ++k) {
       const int x = item_of(k);
       if (x >= p.n_items) continue;
-      const KvItem item = kv_item<WINDOW>(p, x);
+      const KvItem item = kv_item<WINDOW, CUT>(p, x);
       const int j = item.j, i0 = item.i0, nI = item.nI;
       const int key = j * BT + kk;
       const bool key_live = key < p.Sk;
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto grad_row = [&]() { return (r == 0 ? p.dv : p.dk) + (static_cast<int64_t>(item.z) * p.Sk + key) * D; };
       // this warp's rows of the item's fp32 partial dV or dK (window mode)
       auto part_rows = [&]() {
-        return p.sink_part + ((static_cast<int64_t>(item.part) * 2 + r) * BT + quarter * 32) * D;
+        return p.part + ((static_cast<int64_t>(item.part) * 2 + r) * BT + quarter * 32) * D;
       };
       if (nI <= 0) {  // no query row sees this key tile: zero gradients
         if (WINDOW && item.part >= 0) {
@@ -518,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         continue;
       }
-      for (int s = 0; s < G * nI; ++s, ++it, ++g) {
+      for (int s = 0; s < (CUT ? item.nH : G) * nI; ++s, ++it, ++g) {
         const int i = i0 + s % nI;
         const uint8_t* sl = ring + (it % kRing) * C::kSlotBytes;
         const float4* nl4 = reinterpret_cast<const float4*>(sl + 2 * C::kTileBytes) + (BH2 / 4) * r;
@@ -628,10 +639,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Window mode: dV and dK of the key tiles that hold sinks, the partials of their chunks
+// Window mode: dV and dK of the key tiles whose work is cut, the partials of their items
 // added in order.  One thread per four columns of a key's row.
 template <int D>
-__global__ void __launch_bounds__(256) attn_bwd_sink_kernel(const BParams p) {
+__global__ void __launch_bounds__(256) attn_bwd_parts_kernel(const BParams p) {
   griddep_wait();
   const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // [tile][z][dV, dK][key][D / 4]
   const int c4 = static_cast<int>(e % (D / 4));
@@ -640,11 +651,15 @@ __global__ void __launch_bounds__(256) attn_bwd_sink_kernel(const BParams p) {
   const int in = static_cast<int>(row % (2 * BT));
   const int j = static_cast<int>(tz / p.BZ), z = static_cast<int>(tz % p.BZ);
   const int key = j * BT + in % BT;
-  if (j >= p.sink_tiles || key >= p.Sk) return;
+  if (j >= p.n_kt || key >= p.Sk) return;
+  // the tile's items: in kv_item's order
+  const int n_chunked = p.sink_tiles() * p.sink_chunks;
+  const int n = (j < p.sink_tiles() ? p.sink_chunks : 1) * p.head_groups;
+  const int first = (j < p.sink_tiles() ? j * p.sink_chunks : n_chunked + j - p.sink_tiles()) * p.head_groups;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const float* src = p.sink_part + ((static_cast<int64_t>(j) * p.sink_chunks * p.BZ + z) * 2 * BT + in) * D + 4 * c4;
+  const float* src = p.part + ((static_cast<int64_t>(first) * p.BZ + z) * 2 * BT + in) * D + 4 * c4;
 #pragma unroll 4
-  for (int c = 0; c < p.sink_chunks; ++c) {
+  for (int c = 0; c < n; ++c) {
     const float4 v = *reinterpret_cast<const float4*>(src + static_cast<int64_t>(c) * p.BZ * 2 * BT * D);
     acc.x += v.x;
     acc.y += v.y;
@@ -678,7 +693,7 @@ __device__ __forceinline__ WinTiles dq_tiles(const BParams& p, int i) {
   w.n_sink = w.j0 = 0;
   if constexpr (WINDOW) {
     w.j0 = min(max(i * BT + p.diag - p.window + 1, 0) / BT, n_full);
-    w.n_sink = min(p.sink_tiles, w.j0);
+    w.n_sink = min(p.sink_tiles(), w.j0);
     w.n = w.n_sink + n_full - w.j0;
   }
   return w;
@@ -1051,10 +1066,13 @@ int prepare_device(int dev) {
                        reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<128, true>),
                        reinterpret_cast<const void*>(attn_bwd_dq_kernel<128, true>),
                        reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<64, true>),
-                       reinterpret_cast<const void*>(attn_bwd_dq_kernel<64, true>)};
+                       reinterpret_cast<const void*>(attn_bwd_dq_kernel<64, true>),
+                       reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<128, true, true>),
+                       reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<64, true, true>)};
   const int bytes[] = {BCfg<128>::kSmemBytes, QCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes, QCfg<64>::kSmemBytes,
-                       BCfg<128>::kSmemBytes, QCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes, QCfg<64>::kSmemBytes};
-  for (int f = 0; f < 8 && e == cudaSuccess; ++f)
+                       BCfg<128>::kSmemBytes, QCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes, QCfg<64>::kSmemBytes,
+                       BCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes};
+  for (int f = 0; f < 10 && e == cudaSuccess; ++f)
     e = cudaFuncSetAttribute(fns[f], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[f]);
   if (e != cudaSuccess) return cuda_fail(e);
   if (!attn_host::encode_tiled_fn()) return ATTN_ERR_TENSOR_MAP;
@@ -1074,34 +1092,66 @@ int64_t padded_rows(int Sq) { return (static_cast<int64_t>(Sq) + BT - 1) / BT * 
 
 // Window mode: how the dK/dV work of the key tiles that hold sinks is cut.  Such a tile is
 // seen by every later query tile, a tile without sinks by about window / 128 + 2 of them;
-// chunks of that many query tiles (eight at least) make the items about equal.  With many sinks
+// chunks of that many query tiles (eight at least; four where that leaves fewer items than SMs, 102 us
+// instead of 140 for 4 kv heads of 3148 tokens and 130 sinks) make the items about equal.  With many sinks
 // the chunks are longer, so that there are at most kMaxSinkItems (7 per SM) and the partials
 // take 134 MB at most (32768 tokens, 32 / 8 heads, window 1024, 4096 sinks: 6.26 ms, 6.76 with
 // 840 MB of chunks as short as for a few sinks; every key a sink: 19.8 ms, 23.9 with 6.7 GB).
-struct SinkPlan {
-  int tiles, chunks, per;
-  size_t bytes;  // of the fp32 partials
+//
+// Few items (short sequences, few kv heads) are cut by heads as well: into the number of groups
+// with the least time in steps, counted as rounds of the SMs times an item's steps, one more per
+// item, one for writing its partial and two for adding them (forward and backward together: one kv head
+// of 8 query heads, 3029 tokens, window 76, 4 sinks, D 64: 48 us, 125 uncut; 2 of 16, 606 tokens, window
+// 37, 130 sinks: 46 us, 155 uncut).
+struct KvPlan {
+  int tiles, chunks, per;  // key tiles with sinks, items of each, query tiles per item
+  int groups;              // items that each of those, and each other tile, is cut into by heads
+  int64_t items;           // ... in all
+  int64_t parts;           // those that leave fp32 partials
 };
 
 constexpr int kMaxSinkChunks = 64;
 constexpr int kMaxSinkItems = 1024;
+constexpr int64_t kSms = 152;
 
-SinkPlan sink_plan(int64_t BZ, int Sq, int Sk, int D, int window, int sinks) {
-  SinkPlan s;
+KvPlan kv_plan(int64_t BZ, int G, int Sq, int Sk, int window, int sinks) {
+  KvPlan s;
   s.tiles = (std::min(sinks, Sk) + BT - 1) / BT;
   const int n_qt = static_cast<int>(padded_rows(Sq) / BT);
+  const int n_kt = (Sk + BT - 1) / BT;
+  const int reach = window / BT + 2;  // query tiles that see a tile without sinks
   const int most = static_cast<int>(
       std::clamp<int64_t>(kMaxSinkItems / std::max<int64_t>(s.tiles * BZ, 1), 1, kMaxSinkChunks));
-  s.per = std::max({window / BT + 2, 8, (n_qt + most - 1) / most});
-  s.chunks = s.tiles > 0 ? std::max((n_qt + s.per - 1) / s.per, 1) : 1;
-  s.bytes = s.chunks > 1 ? static_cast<size_t>(s.tiles) * s.chunks * BZ * 2 * BT * D * 4 : 0;
+  int64_t base = 0;
+  for (int shortest : {8, 4}) {
+    s.per = std::max({reach, shortest, (n_qt + most - 1) / most});
+    s.chunks = s.tiles > 0 ? std::max((n_qt + s.per - 1) / s.per, 1) : 1;
+    base = (n_kt + static_cast<int64_t>(s.tiles) * (s.chunks - 1)) * BZ;
+    if (base >= kSms) break;
+  }
+  const int64_t longest = std::min(s.tiles > 0 ? s.per : reach, std::max(n_qt, 1));
+  s.groups = 1;
+  int64_t least = (base + kSms - 1) / kSms * (G * longest + 1);
+  for (int heads = G - 1; heads >= 1; --heads) {
+    const int groups = (G + heads - 1) / heads;
+    if (base * groups > 2 * kSms) break;
+    const int64_t steps = (base * groups + kSms - 1) / kSms * (heads * longest + 2) + 2;
+    if (steps < least) {
+      least = steps;
+      s.groups = groups;
+    }
+  }
+  s.items = base * s.groups;
+  s.parts = s.groups > 1 ? s.items : s.chunks > 1 ? static_cast<int64_t>(s.tiles) * s.chunks * BZ : 0;
   return s;
 }
 
+size_t part_bytes(const KvPlan& s, int D) { return static_cast<size_t>(s.parts) * 2 * BT * D * 4; }
+
 template <int D, bool WINDOW>
 int launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tdo,
-               BParams prm, const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse, float* lse2,
-               float* delta, int sms, cudaStream_t stream) {
+               BParams prm, int64_t kv_items, const __nv_bfloat16* o, const __nv_bfloat16* dout, const float* lse,
+               float* lse2, float* delta, int sms, cudaStream_t stream) {
   const int64_t prep_rows = static_cast<int64_t>(prm.BH) * prm.Sq_pad;
   const int64_t prep_warps = (prep_rows + 32 / (D / 8) - 1) / (32 / (D / 8));
   attn_bwd_prep_kernel<D><<<static_cast<unsigned>((prep_warps + 7) / 8), 256, 0, stream>>>(
@@ -1120,21 +1170,25 @@ int launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   BParams a = prm;
-  a.n_items = WINDOW ? (prm.n_kt + prm.sink_tiles * (prm.sink_chunks - 1)) * prm.BZ : prm.n_kt * prm.BZ;
+  a.n_items = static_cast<int>(kv_items);
   cfg.gridDim = dim3(a.n_items < sms ? a.n_items : sms);
-  e = cudaLaunchKernelEx(&cfg, attn_bwd_dkdv_kernel<D, WINDOW>, tq, tk, tv, tdo, a);
+  if (WINDOW && prm.head_groups > 1)
+    e = cudaLaunchKernelEx(&cfg, attn_bwd_dkdv_kernel<D, WINDOW, WINDOW>, tq, tk, tv, tdo, a);
+  else
+    e = cudaLaunchKernelEx(&cfg, attn_bwd_dkdv_kernel<D, WINDOW>, tq, tk, tv, tdo, a);
   if (e != cudaSuccess) return cuda_fail(e);
   BParams b = prm;
   b.n_items = prm.n_qt * prm.BH;
   cfg.gridDim = dim3(b.n_items < sms ? b.n_items : sms);
   cfg.dynamicSmemBytes = QCfg<D>::kSmemBytes;
   e = cudaLaunchKernelEx(&cfg, attn_bwd_dq_kernel<D, WINDOW>, tq, tk, tv, tdo, b);
-  if (WINDOW && e == cudaSuccess && prm.sink_tiles > 0 && prm.sink_chunks > 1) {
-    const int64_t quads = static_cast<int64_t>(prm.sink_tiles) * prm.BZ * 2 * BT * (D / 4);
+  if (WINDOW && e == cudaSuccess && (prm.head_groups > 1 || (prm.sink_tiles() > 0 && prm.sink_chunks > 1))) {
+    const int64_t tiles = prm.head_groups > 1 ? prm.n_kt : prm.sink_tiles();
+    const int64_t quads = tiles * prm.BZ * 2 * BT * (D / 4);
     cfg.gridDim = dim3(static_cast<unsigned>((quads + 255) / 256));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, attn_bwd_sink_kernel<D>, prm);
+    e = cudaLaunchKernelEx(&cfg, attn_bwd_parts_kernel<D>, prm);
   }
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
@@ -1157,8 +1211,9 @@ int run_backward(const void* q, const void* k, const void* v, const void* o, con
   const size_t qb = static_cast<size_t>(B) * Hq * Sq * D * 2, kb = static_cast<size_t>(B) * Hkv * Sk * D * 2;
   const size_t lb = static_cast<size_t>(B) * Hq * Sq * 4;
   const size_t vb = vector_bytes(B, Hq, Sq);
-  const SinkPlan sink = sink_plan(static_cast<int64_t>(B) * Hkv, Sq, Sk, D, window, sinks);
-  const size_t wb = vb + sink.bytes;
+  KvPlan plan{};
+  if (window > 0) plan = kv_plan(static_cast<int64_t>(B) * Hkv, Hq / Hkv, Sq, Sk, window, sinks);
+  const size_t wb = vb + part_bytes(plan, D);
   if (Sq > 0 && (!q || !o || !lse || !dout || !dq)) return ATTN_ERR_NULL_PTR;
   if (Sk > 0 && (!k || !v || !dk || !dv)) return ATTN_ERR_NULL_PTR;
   if (Sq > 0 && Sk > 0 && !workspace) return ATTN_ERR_NULL_PTR;
@@ -1226,18 +1281,19 @@ int run_backward(const void* q, const void* k, const void* v, const void* o, con
   prm.scale = scale;
   prm.window = std::min(window, std::max(Sq, Sk));  // no visible key is further away
   prm.sinks = std::min(sinks, Sk);
-  prm.sink_tiles = sink.tiles;
-  prm.sink_chunks = sink.chunks;
-  prm.sink_per = sink.per;
-  prm.sink_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + vb);
+  prm.sink_chunks = plan.chunks;
+  prm.sink_per = plan.per;
+  prm.head_groups = plan.groups;
+  prm.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + vb);
   const auto* ob = static_cast<const __nv_bfloat16*>(o);
   const auto* gb = static_cast<const __nv_bfloat16*>(dout);
   const int sms = g_dev_sms[dev];
   if (window > 0)
-    return D == 128 ? launch_all<128, true>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, sms, stream)
-                    : launch_all<64, true>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, sms, stream);
-  return D == 128 ? launch_all<128, false>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, sms, stream)
-                  : launch_all<64, false>(tq, tk, tv, tdo, prm, ob, gb, lse, lse2, delta, sms, stream);
+    return D == 128 ? launch_all<128, true>(tq, tk, tv, tdo, prm, plan.items, ob, gb, lse, lse2, delta, sms, stream)
+                    : launch_all<64, true>(tq, tk, tv, tdo, prm, plan.items, ob, gb, lse, lse2, delta, sms, stream);
+  const int64_t items = static_cast<int64_t>(prm.n_kt) * prm.BZ;
+  return D == 128 ? launch_all<128, false>(tq, tk, tv, tdo, prm, items, ob, gb, lse, lse2, delta, sms, stream)
+                  : launch_all<64, false>(tq, tk, tv, tdo, prm, items, ob, gb, lse, lse2, delta, sms, stream);
 }
 
 }  // namespace
@@ -1257,8 +1313,9 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* o, const f
 }
 
 size_t attn_bwd_window_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks) {
-  if (B < 0 || Hq < 1 || Hkv < 1 || Sq < 0 || Sk < 0 || (D != 64 && D != 128) || window < 1 || sinks < 0) return 0;
-  return vector_bytes(B, Hq, Sq) + sink_plan(static_cast<int64_t>(B) * Hkv, Sq, Sk, D, window, sinks).bytes;
+  if (B < 0 || Hq < 1 || Hkv < 1 || Sq < 0 || Sk < 0 || (D != 64 && D != 128) || window < 1 || sinks < 0 || Hq % Hkv != 0)
+    return 0;
+  return vector_bytes(B, Hq, Sq) + part_bytes(kv_plan(static_cast<int64_t>(B) * Hkv, Hq / Hkv, Sq, Sk, window, sinks), D);
 }
 
 int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,

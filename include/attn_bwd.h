@@ -59,8 +59,9 @@ size_t attn_bwd_workspace_size(int B, int Hq, int Sq);
  * that attn_fwd_window's window and sinks leave visible.  o and lse are its outputs for
  * the same q, k, v, causal, window, sinks and scale.  Only tiles that some row sees
  * are loaded.  A key tile that holds sinks is seen by every later query row: its
- * dK and dV work is cut into chunks of query tiles whose fp32 partials lie in the
- * workspace and are added in a fixed order, so results are the same from run to run.
+ * dK and dV work is cut into chunks of query tiles, and where there is little work in all
+ * it is cut by query heads too.  The fp32 partials of what is cut lie in the workspace and
+ * are added in a fixed order, so results are the same from run to run.
  * causal is 1 or 2, window >= 1, sinks >= 0.  Three or four kernels are enqueued;
  * everything else is as attn_bwd.
  */
@@ -68,8 +69,8 @@ int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, 
                     void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Sq, int Sk, int D, int causal,
                     int window, int sinks, float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Workspace bytes attn_bwd_window needs: attn_bwd_workspace_size, and for each key tile
-   that holds sinks up to 64 fp32 dK and dV tiles per kv head; 0 for invalid sizes.  Host only. */
+/* Workspace bytes attn_bwd_window needs: attn_bwd_workspace_size, and fp32 dK and dV tiles of
+   what is cut, at most 1024 of them (D KB each); 0 for invalid sizes.  Host only. */
 size_t attn_bwd_window_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks);
 
 /* Text for a status code (ATTN_ERR_CUDA names this library's last CUDA error on the

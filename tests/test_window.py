@@ -1,7 +1,7 @@
 """Sliding-window attention with sink tokens (attn_fwd_window, attn_bwd_window) against the definition in 64 bits:
 windows of one key up to the whole sequence, windows and sinks that end inside, at and past a 128-key tile, both
 alignments, ragged lengths, grouped heads, rows without keys, and key tiles with sinks whose backward work is cut
-into chunks.
+into chunks, by heads too where there are few.
 
 Tolerances are those of the dense entry points: |dO| <= 1e-2 and |dLSE| <= 1e-3 (parity_util: an output of
 magnitude below 4 is rounded to bf16 by at most 2^-7, P by 2^-12 of itself), and for a gradient the rounding of its
@@ -31,8 +31,11 @@ CASES = [
     (1, 2, 1, 900, 200, 64, 2, 60, 0),         # top-left, rows past every window: no keys
     (1, 2, 1, 900, 200, 128, 2, 60, 7),        # the same rows see the sinks alone
     (1, 2, 2, 200, 900, 64, 2, 33, 1),         # keys no row sees
-    (1, 2, 1, 2500, 2500, 128, 1, 5, 3),       # the sinks' tile in three chunks
-    (1, 4, 1, 2500, 2600, 64, 1, 200, 260),    # three tiles with sinks, each in chunks
+    (1, 2, 1, 2500, 2500, 128, 1, 5, 3),       # the sinks' tile in chunks
+    (1, 4, 1, 2500, 2600, 64, 1, 200, 260),    # three tiles with sinks, each in chunks, cut by heads too
+    (1, 3, 3, 2500, 2500, 128, 1, 5, 3),       # chunks alone: one head per kv head
+    (1, 6, 1, 800, 800, 128, 1, 150, 0),       # cut by heads alone
+    (1, 9, 1, 4500, 4500, 64, 1, 700, 0),      # ... into groups of which the last is shorter
     (1, 4, 2, 900, 900, 128, 1, 100, 16),      # as many sinks as a step of few keys holds, and one more
     (1, 4, 2, 900, 900, 64, 1, 100, 17),
     (1, 3, 1, 900, 900, 64, 1, 300, 16),       # three heads of a group: 256 rows of each
@@ -99,12 +102,14 @@ def test_sharp_logits_move_the_reference_value():
 @pytest.mark.gpu
 @pytest.mark.parametrize("D", [64, 128])
 def test_a_window_over_everything_is_the_dense_call_bitwise(D):
-    q, k, v = [t.cuda() for t in draw(2, 4, 2, 700, 900, D, seed=23)]
-    do = draw(2, 4, 2, 700, 900, D, seed=24)[0].cuda()
-    for causal in (1, 2):
+    for Hkv, causal in ((2, 1), (2, 2), (4, 1), (4, 2)):
+        q, k, v = [t.cuda() for t in draw(2, 4, Hkv, 700, 900, D, seed=23)]
+        do = draw(2, 4, Hkv, 700, 900, D, seed=24)[0].cuda()
         dense = ops.attn_fwd(q, k, v, causal=causal)
         near = ops.attn_fwd_window(q, k, v, 900, causal=causal)
         assert all(torch.equal(a, b) for a, b in zip(dense, near))
+        if Hkv == 2:  # so few items are cut by heads, and the heads' sums are added in another order
+            continue
         a = ops.attn_bwd(q, k, v, *dense, do, causal=causal)
         b = ops.attn_bwd_window(q, k, v, *near, do, 900, causal=causal)
         assert all(torch.equal(x, y) for x, y in zip(a, b))
@@ -239,9 +244,12 @@ def test_pointers_and_workspace():
     assert fwd(o=O + 4) == ops.ATTN_ERR_MISALIGNED
     assert fwd(o=K) == ops.ATTN_ERR_INVALID_ARG
     lib = _lib.load("attn_bwd")
+    need = ops.bwd_window_workspace_size(1, 4, 4, 2500, 2500, 128, 5, 3)
+    # -LSE and -D of 2560 rows of four heads, then dV and dK of the one tile with sinks: 5 chunks of 4 query tiles
+    assert need == 2 * 4 * 2560 * 4 + 5 * 4 * 2 * 128 * 128 * 4
+    # two heads per kv head: each of the 24 items of a kv head is cut in two
     need = ops.bwd_window_workspace_size(1, 4, 2, 2500, 2500, 128, 5, 3)
-    # -LSE and -D of 2560 rows of four heads, then dV and dK of the one tile with sinks: 3 chunks of 8 query tiles
-    assert need == 2 * 4 * 2560 * 4 + 3 * 2 * 2 * 128 * 128 * 4
+    assert need == 2 * 4 * 2560 * 4 + 2 * 24 * 2 * 2 * 128 * 128 * 4
     bwd = lambda ws=0x9000000, n=need: lib.attn_bwd_window(  # noqa: E731
         0x1000000, 0x2000000, 0x3000000, 0x4000000, 0x5000000, 0x6000000, 0x7000000, 0x8000000, 0x8800000, 1, 4, 2,
         2500, 2500, 128, 1, 5, 3, 0.1, ws, n, None)
@@ -252,7 +260,7 @@ def test_pointers_and_workspace():
     for sinks in (1024, 4096, 32768, 2 ** 31 - 1):
         size = ops.bwd_window_workspace_size(1, 32, 8, 32768, 32768, 128, 1024, sinks)
         assert 0 <= size - 2 * 32 * 32768 * 4 <= 1024 * 2 * 128 * 128 * 4
-    for bad in (dict(window=0), dict(sinks=-1), dict(D=96), dict(Hkv=0)):
+    for bad in (dict(window=0), dict(sinks=-1), dict(D=96), dict(Hkv=0), dict(Hkv=3)):
         a = dict(dict(B=1, Hq=4, Hkv=2, Sq=64, Sk=64, D=128, window=8, sinks=2), **bad)
         assert lib.attn_bwd_window_workspace_size(*a.values()) == 0
 
