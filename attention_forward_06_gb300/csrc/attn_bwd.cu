@@ -36,6 +36,7 @@
 #include "attn_bwd.h"
 #include "host_util.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 using namespace attn;
 
@@ -155,41 +156,6 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ void record_abort(volatile uint32_t* abort_flag, int site) {
   *abort_flag = 1;
   atomicCAS(&g_bwd_status, 0, site);
-}
-
-// Stores 32 rows of a warp, one row per lane (lane m holds its row's CH 16-byte chunks in
-// w[0 .. 4 CH)), row m at base + m * stride; rows m >= live_rows are skipped.  A warp store
-// of one 16-byte chunk per lane would touch 32 rows (32 cache lines); instead the chunks are
-// transposed within each group of CH lanes (log2 CH butterfly stages of shuffles, each
-// swapping one bit between lane and chunk index), after which lane CH g + q holds chunk q of
-// rows CH g .. CH g + CH - 1, and each of the CH stores writes 32 / CH whole rows.
-template <int CH>
-__device__ __forceinline__ void store_warp_rows(uint32_t (&w)[4 * CH], uint8_t* base, int64_t stride, int live_rows,
-                                                int lane) {
-  const int q = lane % CH;
-#pragma unroll
-  for (int b = CH / 2; b >= 1; b /= 2) {
-    const bool hi = (q & b) != 0;
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      if (c & b) continue;
-#pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const uint32_t send = hi ? w[4 * c + h] : w[4 * (c ^ b) + h];
-        const uint32_t recv = __shfl_xor_sync(0xffffffffu, send, b);
-        if (hi)
-          w[4 * c + h] = recv;
-        else
-          w[4 * (c ^ b) + h] = recv;
-      }
-    }
-  }
-  const int m0 = lane - q;
-#pragma unroll
-  for (int k = 0; k < CH; ++k)
-    if (m0 + k < live_rows)
-      *reinterpret_cast<uint4*>(base + (m0 + k) * stride + 16 * q) =
-          make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
 }
 
 // ---------------------------------------------------------------------------- prep
@@ -1313,9 +1279,11 @@ int attn_bwd(const void* q, const void* k, const void* v, const void* o, const f
 }
 
 size_t attn_bwd_window_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks) {
-  if (B < 0 || Hq < 1 || Hkv < 1 || Sq < 0 || Sk < 0 || (D != 64 && D != 128) || window < 1 || sinks < 0 || Hq % Hkv != 0)
+  if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 0 || Sk < 0 || (D != 64 && D != 128) || window < 1 ||
+      sinks < 0)
     return 0;
-  return vector_bytes(B, Hq, Sq) + part_bytes(kv_plan(static_cast<int64_t>(B) * Hkv, Hq / Hkv, Sq, Sk, window, sinks), D);
+  const KvPlan plan = kv_plan(static_cast<int64_t>(B) * Hkv, Hq / Hkv, Sq, Sk, window, sinks);
+  return vector_bytes(B, Hq, Sq) + part_bytes(plan, D);
 }
 
 int attn_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,

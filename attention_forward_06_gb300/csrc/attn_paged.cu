@@ -22,9 +22,10 @@
 //               slots of V and arrive late: 404 us where this takes 240)
 //   warp  11    TMA of the Q rows
 // Pairs (PAIR).  With more tokens than a row tile holds an item is two row tiles that share
-// each K and V tile: warps 0-3 and 4-7 take one each and convert half of V each.  Eight
-// trees of 32 to 64 tokens, 4 heads per kv head, up to 16384 keys, D 128: 127 us, against
-// 152 with the row tiles apart, which read K and V twice.
+// each K and V tile: warps 0-3 and 4-7 take one each and convert half of V each (with four
+// more warps that convert, 128 us for 127: the conversion is done while S is on its way).
+// Eight trees of 32 to 64 tokens, 4 heads per kv head, up to 16384 keys, D 128: 113 us
+// (152 for 127 with the row tiles apart, which read K and V twice).
 // Key groups.  A thread of a softmax warp sees one TMEM lane, one row; with 32 rows or
 // fewer (a token or a few per sequence) three of the four warps would idle while one takes
 // the exponentials of all 128 keys.  So such an item's rows are repeated in the lanes of all four
@@ -39,15 +40,19 @@
 // largest key starts at 2^6 and fp16 keeps keys down to 2^-20 of it in full precision, 2^-30 at
 // all.  Later tiles are taken against the same m, without their max; where 32 keys' sum of P
 // passes fp16's largest value m moves to 6 below their max, and P, the sums and O (in TMEM,
-// once the PV before has finished) are scaled.
+// once the PV before has finished) are scaled.  One sum, of the fp32 P, gives LSE and
+// normalises O: each P in fp16 is off by 2^-12 of itself at most, an eighth of O's rounding to
+// bf16, and a second sum over the rounded P costs four of nine instructions (122 us for 116).
 //
 // Measured (graph of 20 calls, both kernels): 64 sequences of up to 8192 keys, one token each,
-// 32 / 8 heads, D 128: 240 us, 6.8 TB/s of K and V, the card's copy rate.  32 sequences, a window
-// of 4096 and 4 sinks, 16 heads, D 64: 109 us (4.9 TB/s: items of 33 tiles, whose ends show).
-// One token over 2048 keys: 14.8 us, the latency of the plan, two loads, a tile and the merge.
-// The loops over columns and chunks are rolled: with twelve warps of five kinds the instruction
-// cache is what unrolled code waits for (the trees took 210 us with 64 columns at a time, 163
-// with 32).
+// 32 / 8 heads, D 128: 240 us, 6.8 TB/s of K and V, the card's copy rate.  32 sequences, a
+// window of 4096 and 4 sinks, 16 heads, D 64: 102 us (5.3 TB/s: items of 33 tiles, whose ends
+// show).  One token over 2048 keys: 14.4 us, the latency of the plan, two loads, a
+// tile and the merge.
+// What bounds the rest is the reaction of the roles to one another: with twelve warps of
+// five kinds an instruction that a warp has not run for a step is fetched anew, 8 at a time, some
+// 60 cycles each.  So the loops over columns and chunks are rolled (the trees took 210 us with
+// 64 columns at a time, 163 with 32), and the issuer's path is short (below).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -62,6 +67,7 @@
 #include "host_util.h"
 #include "kv_host.h"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 using namespace attn;
 
@@ -120,6 +126,7 @@ struct Params {
   const uint32_t* mask;  // [tokens][mask_words] or null (a chain)
   int mask_words;
   int rows, max_pages, n_pages, page_size;  // rows: sequences
+  int page_shift;  // page_size == 1 << page_shift
   int n_tokens, Hq, Hkv, G;
   int R;  // tokens per row tile: BM / G
   int item_tokens;  // R, or 2 R where an item is a pair of row tiles
@@ -453,19 +460,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Loads the pages of an item's key tiles, step by step, through a ring of tile slots (both TMA
   // warps; `n` counts the loads of the launch).  Lane i of the window of 32 page numbers that the
   // warp holds loads page i.
-  const int per_tile = p.page_size >= BN ? 1 : BN / p.page_size;  // pages of a tile
+  const int per_tile = p.page_size >= BN ? 1 : BN >> p.page_shift;  // pages of a tile
   const int box_rows = min(p.page_size, BN);
   auto stream = [&](const Item& item, const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty,
                     uint32_t slots, uint32_t& n) -> bool {
     const int32_t* row = p.table + static_cast<int64_t>(item.b) * p.max_pages;
-    const int used = (item.kv_len + p.page_size - 1) / p.page_size;
+    const int used = (item.kv_len + p.page_size - 1) >> p.page_shift;
     auto load_ids = [&](int w) { return w + lane < used ? __ldg(row + w + lane) : 0; };
     int win = -64, ids = 0, ids_next = 0;  // pages [win, win + 32) of the row, and the next 32 on their way
     for (int s = item.s0; s < item.s1; ++s, ++n) {
       const int key0 = item.tile(s) * BN;
-      const int page0 = key0 / p.page_size, slot0 = key0 % p.page_size;
-      if (page0 / 32 * 32 != win) {
-        const int w = page0 / 32 * 32;
+      const int page0 = key0 >> p.page_shift, slot0 = key0 & (p.page_size - 1);
+      const int w = page0 / 32 * 32;
+      if (w != win) {
         ids = w == win + 32 ? ids_next : load_ids(w);
         ids_next = load_ids(w + 32);
         win = w;
@@ -650,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       struct Walk {
         Item item;
         int k, s, t, tiles;
+        bool grouped;
         uint32_t q, n;
       };
       auto enter = [&](Walk& w) {  // the walk's next item has been published; none: item.s1 == 0
@@ -657,6 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.s = w.item.s0;
         w.t = 0;
         w.tiles = PAIR ? w.item.row_tiles(p.R) : 1;
+        w.grouped = w.item.groups(p.G) > 1;
       };
       auto advance = [&](Walk& w) {
         ++w.q;
@@ -676,43 +685,63 @@ __global__ void __launch_bounds__(kThreads, 1)
       a.item.s1 = b.item.s1 = a.s = b.s = 1;
       uint32_t n_out[2] = {0, 0};  // items whose O went through each accumulator
       uint64_t idle_since = 0;
-      // Whichever of the next S and the next PV has its operands is issued; neither waits for the other's.
+      uint32_t polls = 0;
+      // Whether S(a.q) has its operands (K of a new step, Q of a new item).
+      auto s_ready = [&]() {
+        if (a.item.s1 == 0) return false;
+        if (a.s == a.item.s1) {
+          if (!next_is_out(a)) return false;
+          enter(a);
+          if (a.item.s1 == 0) return false;
+        }
+        if (PAIR && a.t > 0) return true;
+        return is_done(&k_full[a.n % KS], (a.n / KS) & 1) && (a.s > a.item.s0 || is_done(&q_full, a.k & 1));
+      };
+      auto issue_s = [&]() {
+        const uint32_t slot = a.n % KS;
+        const uint64_t qd = sdesc_sw128(opaque(q_addr) + a.t * C::kTileBytes, 16, 1024);
+        const uint64_t kd = sdesc_sw128(opaque(k_addr) + slot * C::kTileBytes, 16, 1024);
+        const uint32_t free_k = a.t + 1 == a.tiles ? smem_u32(&k_empty[slot]) : kNoBar;
+        if constexpr (D == 128)
+          mma_bf16_ss_k8(tmem + (a.q & 1) * BN, qd, kd, idesc_s, smem_u32(&s_full[a.q & 1]), free_k);
+        else
+          mma_bf16_ss_k4(tmem + (a.q & 1) * BN, qd, kd, idesc_s, smem_u32(&s_full[a.q & 1]), free_k);
+        if (a.t + 1 == a.tiles && a.s + 1 == a.item.s1) mma_commit_elect(&q_empty);  // the item's last S
+        advance(a);
+      };
+      // Whichever of the next S and the next PV has its operands is issued; neither waits for the other's
+      // (K of a cache arrives late more often than not).  The code is in the order in which it runs in
+      // the steady state, PV and then the S that it frees, and tests are few: with S first, a clock read per
+      // poll and one vote per test the trees took 127 us for 120, the window 109 for 102.
       while (b.item.s1 > 0) {
         bool idle = true;
-        if (a.item.s1 > 0 && a.q < b.q + 2) {
-          if (a.s == a.item.s1 && next_is_out(a)) enter(a);
-          if (a.s < a.item.s1 && (a.t > 0 || ((a.s > a.item.s0 || is_done(&q_full, a.k & 1)) &&
-                                              is_done(&k_full[a.n % KS], (a.n / KS) & 1)))) {
-            tc_fence_after();
-            const uint32_t slot = a.n % KS;
-            const uint64_t qd = sdesc_sw128(opaque(q_addr) + a.t * C::kTileBytes, 16, 1024);
-            const uint64_t kd = sdesc_sw128(opaque(k_addr) + slot * C::kTileBytes, 16, 1024);
-            const uint32_t free_k = a.t + 1 == a.tiles ? smem_u32(&k_empty[slot]) : kNoBar;
-            if constexpr (D == 128)
-              mma_bf16_ss_k8(tmem + (a.q & 1) * BN, qd, kd, idesc_s, smem_u32(&s_full[a.q & 1]), free_k);
-            else
-              mma_bf16_ss_k4(tmem + (a.q & 1) * BN, qd, kd, idesc_s, smem_u32(&s_full[a.q & 1]), free_k);
-            if (a.t + 1 == a.tiles && a.s + 1 == a.item.s1) mma_commit_elect(&q_empty);  // the item's last S
-            advance(a);
-            idle = false;
-          }
-        }
         if (b.s == b.item.s1 && next_is_out(b)) enter(b);
-        if (b.s < b.item.s1 && b.q < a.q && is_done(&p_full[b.q & 1], (b.q >> 1) & 1) &&
-            (b.t > 0 || is_done(&v_ready[b.n % kReady], (b.n / kReady) & 1))) {
+        if (b.s < b.item.s1 && b.q < a.q) {
           const bool first = b.s == b.item.s0, last = b.s + 1 == b.item.s1;
           const uint32_t outs = b.t == 0 ? n_out[0] : n_out[1];
-          if (!first || outs == 0 || is_done(&o_empty[b.t], (outs - 1) & 1)) {
+          // With no S to issue before it a pair has but P to wait for, and a wait reacts sooner than the
+          // polls (120 us for 124); single row tiles are better off without (102 us, 106 with it).
+          if (PAIR && a.q == b.q + 2 && !warp_wait(&p_full[b.q & 1], (b.q >> 1) & 1, abort_v, kTimeoutNs)) {
+            ok = false;
+            break;
+          }
+          bool ready = mbar_test(&p_full[b.q & 1], (b.q >> 1) & 1);
+          if (!PAIR || b.t == 0) ready &= mbar_test(&v_ready[b.n % kReady], (b.n / kReady) & 1);
+          if (first && outs > 0) ready &= mbar_test(&o_empty[b.t], (outs - 1) & 1);
+          if (__all_sync(0xffffffffu, ready)) {
             tc_fence_after();
+            // asked before, so that S follows at once (a pair's P has waited long enough: 131 us for 120)
+            const bool with_s = !PAIR && s_ready();
             const uint32_t slot = b.n % VS;
             const uint64_t vd = sdesc_sw128(opaque(v_addr) + slot * C::kTileBytes, C::kColBlockBytes, 1024);
             // with key groups the epilogue uses the last V slot as its stage and hands it back itself
-            const bool keep = b.t + 1 < b.tiles || (last && b.item.groups(p.G) > 1);
+            const bool keep = b.t + 1 < b.tiles || (last && b.grouped);
             mma_bf16_ts_k8(tmem + kTmemO + b.t * D,
                            tmem + (C::kOverS ? (b.q & 1) * BN : kTmemP + (b.q & 1) * (BN / 2)), vd, idesc_pv,
                            first ? 0u : 1u, smem_u32(&pv_done), keep ? kNoBar : smem_u32(&v_empty[slot]));
+            if (last) mma_commit_elect(&o_full[b.t]);  // the row tile's O is complete
+            if (with_s) issue_s();
             if (last) {
-              mma_commit_elect(&o_full[b.t]);  // the row tile's O is complete
               if (b.t == 0)
                 ++n_out[0];
               else
@@ -722,10 +751,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             idle = false;
           }
         }
+        if (a.q < b.q + 2 && s_ready()) {
+          issue_s();
+          idle = false;
+        }
         if (!idle) {
           idle_since = 0;
           continue;
         }
+        if (++polls % 64 != 0) continue;
         const uint64_t now = global_timer_ns();
         if (idle_since == 0) idle_since = now;
         if (__any_sync(0xffffffffu, *abort_v || now - idle_since > kTimeoutNs)) {
@@ -801,8 +835,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // What a thread keeps of its row of a row tile.
     struct Row {
       float m;        // reference value, log2 units
-      float l;        // sum of the fp16-rounded P (normalises O)
-      float l_exact;  // sum of the fp32 P (gives LSE)
+      float l;        // sum of the fp32 P
       int lo, hi;     // the row sees keys [lo, hi), the sinks below hi, and the drafted tokens of `words`
       const uint32_t* words;
       int flags;  // kLive: a row of the item; kNan: it sees a key whose V holds a NaN; kSeen: every row of
@@ -830,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto start = [&]() {
         Row r;
         r.m = -INFINITY;
-        r.l = r.l_exact = 0.0f;
+        r.l = 0.0f;
         r.lo = 0;
         const bool live = row < min(p.R, item.ntok - t * p.R) * p.G;
         r.flags = live ? kLive : 0;
@@ -931,41 +964,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!__any_sync(0xffffffffu, live && cur.m == -INFINITY)) cur.flags |= kSeen;
           }
           // P against m into TMEM, 32 keys at a time, and its sums
-          float sum = 0.0f, sum_exact = 0.0f;
+          float sum = 0.0f;
 #pragma unroll 1
           for (int col = 0; col < n_cols; col += 32) {
             uint32_t r[32], pk[16];
             load_s(col, r);
-            float part, part_exact;
+            float part;
             auto exponentials = [&]() {
               const float neg_m = cur.m == -INFINITY ? 0.0f : -cur.m;
               const uint64_t nm2 = f2_pack(neg_m, neg_m);
               uint64_t e0 = f2_pack(0.0f, 0.0f), e1 = e0;
-              float q0 = 0.0f, q1 = 0.0f, q2 = 0.0f, q3 = 0.0f;
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
                 float x0, x1;
                 f2_unpack(ffma2(f2_pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), c2, nm2), x0, x1);
                 const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                 pk[e] = pack_f16x2(p0, p1);
-                if (e & 1) {
+                if (e & 1)
                   e1 = fadd2(e1, f2_pack(p0, p1));
-                  add_f16x2_to_f32(q2, q3, pk[e]);
-                } else {
+                else
                   e0 = fadd2(e0, f2_pack(p0, p1));
-                  add_f16x2_to_f32(q0, q1, pk[e]);
-                }
               }
               float a0, a1, b0, b1;
               f2_unpack(e0, a0, a1);
               f2_unpack(e1, b0, b1);
-              part_exact = (a0 + a1) + (b0 + b1);
-              part = (q0 + q1) + (q2 + q3);
+              part = (a0 + a1) + (b0 + b1);
             };
             exponentials();
             // Rare: P may have passed fp16's largest value (a NaN fails the comparison too).  m moves to 6
             // below these keys' max; what the tile has of P and of its sums is scaled like O.
-            const bool over = live && !(part_exact <= kF16Max);
+            const bool over = live && !(part <= kF16Max);
             if (__any_sync(0xffffffffu, over)) {
               const float m_new = max_of(r) * c - kStart;
               float a = 1.0f;
@@ -975,7 +1003,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               alpha *= a;
               sum *= a;
-              sum_exact *= a;
               for (int done = 0; done < col; done += 32) {
                 const uint32_t at = p_tmem + (grp * n_cols + done) / 2;
                 tmem_wait_st();
@@ -987,12 +1014,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               exponentials();
             }
             sum += part;
-            sum_exact += part_exact;
             tmem_st16(p_tmem + (grp * n_cols + col) / 2, pk);
           }
           if (__any_sync(0xffffffffu, alpha != 1.0f)) {
             cur.l *= alpha;
-            cur.l_exact *= alpha;
             if (s > item.s0) {
               // O is scaled once PV of the last step is complete.  With two row tiles that is q - 2, and
               // S(q) came after it.  With one it is q - 1, and PV(q) waits for this warp, so that the
@@ -1017,7 +1042,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           cur.l += sum;
-          cur.l_exact += sum_exact;
           if (NG > 1 && (C::kOverS || s - item.s0 < 2)) {
             // P of the other groups' keys: 0.  Columns of their own keep it for the whole item.
             uint32_t zero[16];
@@ -1044,7 +1068,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = cur.flags & kLive;
         const int rows = min(p.R, item.ntok - t * p.R) * p.G;
         const uint32_t o_tmem = tmem + lane_off + kTmemO + t * D;
-        if (cur.flags & kNan) cur.l = __int_as_float(0x7FC00000);
+        const float l_nan = cur.flags & kNan ? __int_as_float(0x7FC00000) : cur.l;  // O of a row that sees a NaN is NaN
         // where a row's result goes: element `at` x D of o, or of the partials
         auto place = [&](int r) {
           const int u = token_of(p, r);
@@ -1059,43 +1083,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (NG == 1) {
           // l is NaN when S or P was; a row without keys has l == 0, and its O is 0 (P was)
-          const float inv = cur.l == 0.0f ? 0.0f : 1.0f / cur.l;
-          const int64_t at = place(row);
+          const float inv = l_nan == 0.0f ? 0.0f : 1.0f / l_nan;
           if (__any_sync(0xffffffffu, live)) {
+            // whole rows per store (a row per lane took 3 us longer per item, 116 us in all for 113)
+            const int live_rows = rows - quarter * 32;
+            const int m0 = lane / 4 * 4;  // bf16: this lane stores a chunk of the rows m0 .. m0 + 3
+            int64_t at[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) at[k] = whole ? place(quarter * 32 + m0 + k) * D + lane % 4 * 8 : 0;
+            uint8_t* part = reinterpret_cast<uint8_t*>(p.part_o + (whole ? 0 : place(quarter * 32) * D));
 #pragma unroll 1
             for (int cb = 0; cb < D / 32; ++cb) {
               uint32_t o[32];
               tmem_ld32_wait(o_tmem + 32 * cb, o);
 #pragma unroll
               for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * inv);
-              if (live && whole) {
-                uint4* dst = reinterpret_cast<uint4*>(p.o + at * D + 32 * cb);
+              if (whole) {
+                uint32_t w[16];
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                  uint32_t w[4];
+                for (int e = 0; e < 16; ++e)
+                  w[e] = pack_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+                transpose_chunks<4>(w, lane);
 #pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    w[e] = pack_bf16x2(__uint_as_float(o[8 * ch + 2 * e]), __uint_as_float(o[8 * ch + 2 * e + 1]));
-                  dst[ch] = make_uint4(w[0], w[1], w[2], w[3]);
-                }
-              } else if (live) {
-                uint4* dst = reinterpret_cast<uint4*>(p.part_o + at * D + 32 * cb);
-#pragma unroll
-                for (int ch = 0; ch < 8; ++ch)
-                  dst[ch] = make_uint4(o[4 * ch], o[4 * ch + 1], o[4 * ch + 2], o[4 * ch + 3]);
+                for (int k = 0; k < 4; ++k)
+                  if (m0 + k < live_rows)
+                    *reinterpret_cast<uint4*>(p.o + at[k] + 32 * cb) =
+                        make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+              } else {
+                store_warp_rows<8>(o, part + 128 * cb, 4 * D, live_rows, lane);
               }
             }
           }
           tc_fence_before();
           mbar_arrive(&o_empty[t]);  // the next item's first PV may overwrite O
-          if (live) put_lse(cur.l == 0.0f ? -INFINITY : cur.m + lg2_approx(cur.l_exact));
+          if (live) put_lse(cur.l == 0.0f ? -INFINITY : cur.m + lg2_approx(cur.l));
         } else {
           // The groups' sums of a row, each against its own m, are joined in the last V slot, which the
           // issuer left to the epilogue: m and the sums in its last 2 KB, O below them, in two halves
           // of the columns if there is not room for all.
           uint8_t* stage = v_s + ((g - 1) % VS) * C::kTileBytes;
           float4* stat = reinterpret_cast<float4*>(stage + C::kTileBytes - BM * 16);
-          stat[grp * kRows + row] = make_float4(cur.m, cur.l, cur.l_exact, 0.0f);
+          stat[grp * kRows + row] = make_float4(cur.m, l_nan, cur.l, 0.0f);
           if (!join()) return false;
           float m_all = -INFINITY, l_all = 0.0f, x_all = 0.0f;
 #pragma unroll
@@ -1429,13 +1457,14 @@ int attn_fwd_tree(const attn_kv_cache* cache, const void* q, int64_t q_stride_to
   p.max_pages = c.max_pages;
   p.n_pages = c.n_pages;
   p.page_size = c.page_size;
+  p.page_shift = __builtin_ctz(static_cast<unsigned>(c.page_size));
   p.n_tokens = n_tokens;
   p.Hq = Hq;
   p.Hkv = c.Hkv;
   p.G = Hq / c.Hkv;
   p.R = BM / p.G;
   // Pairs of row tiles, which share each key tile, when the sequences have more tokens than a row tile
-  // on average (127 us instead of 152, see the head).  With fewer the second softmax warps would only
+  // on average (see the head).  With fewer the second softmax warps would only
   // convert, and V has a slot less: one token each, 272 us instead of 240 (D 128), 135 instead of 109 (D 64).
   p.item_tokens = n_tokens > static_cast<int64_t>(p.R) * c.rows ? 2 * p.R : p.R;
   p.G_inv = (65536u + p.G - 1) / p.G;
