@@ -28,7 +28,7 @@
 // Window mode (WINDOW): the same kernels over the tiles that the window and the sinks leave
 // visible, and a fourth, attn_bwd_parts_kernel, that adds the fp32 partials of key tiles whose
 // work is cut.  Measured: 16384 tokens, 32 / 8 heads, D 128, window 1024, 4 sinks: prep 43 us,
-// dK/dV 489, dQ 329, parts 6; the steps take what they take in the dense mode (1.82 and 1.22 us
+// dK/dV 489, dQ 319, parts 6; the steps take what they take in the dense mode (1.82 and 1.22 us
 // per 128 x 128 tile), 9 or 10 tiles are visited for 8 tiles' worth of keys.  2 x 1000 tokens, 16 heads, D
 // 64, window 200, forward included: 44 us, the latency of four kernels of short items.
 #include <cuda.h>
@@ -643,10 +643,15 @@ __global__ void __launch_bounds__(256) attn_bwd_parts_kernel(const BParams p) {
   *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
 }
 
+// Window mode: keys of a step for a few sinks, one K step of the MMA (16384 tokens, 32 / 8 heads, D 128,
+// window 1024, 4 sinks, forward and backward: 1098 us, 1108 with the whole tile).
+constexpr int kFewKeys = 16;
+
 // Window mode: the key tiles query tile i visits, those that hold sinks and are before
 // its window, then the window's.
 struct WinTiles {
   int n, n_sink, j0;
+  bool few;  // the first tile is there for its sinks alone (with at most kFewKeys a short step)
   __device__ __forceinline__ int tile(int s) const { return s < n_sink ? s : j0 + s - n_sink; }
 };
 
@@ -664,10 +669,12 @@ __device__ __forceinline__ WinTiles dq_tiles(const BParams& p, int i) {
   const int n_full = key_tiles(p, i);
   w.n = n_full;
   w.n_sink = w.j0 = 0;
+  w.few = false;
   if constexpr (WINDOW) {
     w.j0 = min(max(i * BT + p.diag - p.window + 1, 0) / BT, n_full);
     w.n_sink = min(p.sink_tiles(), w.j0);
     w.n = w.n_sink + n_full - w.j0;
+    w.few = w.n_sink == 1;
   }
   return w;
 }
@@ -692,7 +699,8 @@ struct QCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
-template <int D, bool WINDOW = false>
+// FEW (window mode): with at most kFewKeys sinks their tile is a step of those keys alone.
+template <int D, bool WINDOW = false, bool FEW = false>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_bwd_dq_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                        const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
@@ -809,32 +817,38 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t q_addr = smem_u32(q_s), do_addr = smem_u32(do_s);
     const uint32_t k_addr = smem_u32(k_ring), v_addr = smem_u32(v_ring);
     // S = Q K^T into TMEM region `reg`
-    auto issue_s = [&](uint32_t reg, uint32_t ks) {
+    constexpr uint32_t idesc_few = idesc_bf16_f32(BT, kFewKeys, false);
+    auto issue_s = [&](uint32_t reg, uint32_t ks, bool few) {
       const uint64_t qd = sdesc_sw128(q_addr, 16, 1024);
       const uint64_t kd = sdesc_sw128(opaque(k_addr) + ks * C::kTileBytes, 16, 1024);
       if constexpr (D == 128)
-        mma_bf16_ss_k8(tmem + reg, qd, kd, idesc_s);
+        mma_bf16_ss_k8(tmem + reg, qd, kd, FEW && few ? idesc_few : idesc_s);
       else
-        mma_bf16_ss_k4(tmem + reg, qd, kd, idesc_s);
+        mma_bf16_ss_k4(tmem + reg, qd, kd, FEW && few ? idesc_few : idesc_s);
     };
     // dP = dO V^T; the step's S and dP are then ready, and V is free
-    auto issue_dp = [&](uint32_t vs) {
+    auto issue_dp = [&](uint32_t vs, bool few) {
       const uint64_t dod = sdesc_sw128(do_addr, 16, 1024);
       const uint64_t vd = sdesc_sw128(opaque(v_addr) + vs * C::kTileBytes, 16, 1024);
       if constexpr (D == 128)
-        mma_bf16_ss_k8(tmem + kDp, dod, vd, idesc_s, smem_u32(&st_full), smem_u32(&vempty[vs]));
+        mma_bf16_ss_k8(tmem + kDp, dod, vd, FEW && few ? idesc_few : idesc_s, smem_u32(&st_full), smem_u32(&vempty[vs]));
       else
-        mma_bf16_ss_k4(tmem + kDp, dod, vd, idesc_s, smem_u32(&st_full), smem_u32(&vempty[vs]));
+        mma_bf16_ss_k4(tmem + kDp, dod, vd, FEW && few ? idesc_few : idesc_s, smem_u32(&st_full), smem_u32(&vempty[vs]));
     };
     // dQ += dS K for step gg (dS in region gg & 1, K in slot ks), one 64-key half per
     // warpgroup as its dS arrives; the item's first step overwrites dQ once the previous
     // item's epilogue has read it, its last commits acc_full; K is free afterwards
-    auto issue_acc = [&](uint32_t gg, uint32_t ks, bool first, bool last, uint32_t tt) -> bool {
+    auto issue_acc = [&](uint32_t gg, uint32_t ks, bool first, bool last, uint32_t tt, bool few) -> bool {
       const uint32_t reg = tmem + BT * (gg & 1), ka = opaque(k_addr) + ks * C::kTileBytes;
       bool w = warp_wait(&ds_full[0][gg & 1], (gg >> 1) & 1, abort_v, kTimeoutNs);
       if (w && first && tt > 0) w = warp_wait(&acc_empty, (tt - 1) & 1, abort_v, kTimeoutNs);
       if (!w) return false;
       tc_fence_after();
+      if (FEW && few) {  // its keys are in half 0
+        mma_bf16_ts_k1(tmem + kDq, reg, sdesc_sw128(ka, BC::kColBlockBytes, 1024), idesc_acc, 0u,
+                       smem_u32(&kempty[ks]), last ? smem_u32(&acc_full) : kNoBar);
+        return warp_wait(&ds_full[1][gg & 1], (gg >> 1) & 1, abort_v, kTimeoutNs);
+      }
       mma_bf16_ts_k4(tmem + kDq, reg, sdesc_sw128(ka, BC::kColBlockBytes, 1024), idesc_acc, first ? 0u : 1u);
       ATTN_TR(11, (first ? 0u : 1u) | (last ? 2u : 0u));  // half 0's dQ += dS K (arg: item's first, last)
       w = warp_wait(&ds_full[1][gg & 1], (gg >> 1) & 1, abort_v, kTimeoutNs);
@@ -851,11 +865,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0, t = 0;    // steps (= K and V tiles), items with key tiles
     uint32_t pk = 0, pt = 0;  // the step whose dQ += dS K is pending: K slot, item
     int pj = -1, pn = 0;      // ... and its index within the item, the item's steps
+    bool pfew = false;        // ... and whether it is one of few keys
     bool ok = true;
     for (int k = 0; k * static_cast<int>(gridDim.x) < p.n_items && ok; ++k) {
       const int x = item_of(k);
       if (x >= p.n_items) continue;
-      const int n = dq_tiles<WINDOW>(p, p.n_qt - 1 - x / p.BH).n;
+      const WinTiles wt = dq_tiles<WINDOW>(p, p.n_qt - 1 - x / p.BH);
+      const int n = wt.n;
       if (n <= 0) continue;
       ok = warp_wait(&qd_full, t & 1, abort_v, kTimeoutNs);
       for (int j = 0; j < n && ok; ++j, ++g) {
@@ -864,14 +880,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (j == 0) ATTN_TR(10, x);  // the item's first S product
-        issue_s(BT * (g & 1), ks);
+        issue_s(BT * (g & 1), ks, wt.few && j == 0);
         if (g > 0) ok = warp_wait(&dp_free, (g - 1) & 1, abort_v, kTimeoutNs);  // dP(g-1) read by all
         if (ok) ok = warp_wait(&vfull[vs], (g / VR) & 1, abort_v, kTimeoutNs);
         if (!ok) break;
         tc_fence_after();
-        issue_dp(vs);
+        issue_dp(vs, wt.few && j == 0);
         if (j + 1 == n) mma_commit_elect(&qd_empty);  // Q and dO are read only by S and dP
-        if (pj >= 0) ok = issue_acc(g - 1, pk, pj == 0, pj + 1 == pn, pt);
+        if (pj >= 0) ok = issue_acc(g - 1, pk, pj == 0, pj + 1 == pn, pt, pfew);
+        if constexpr (FEW) pfew = wt.few && j == 0;
         pk = ks;
         pj = j;
         pn = n;
@@ -880,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ++t;
     }
-    if (ok && pj >= 0) ok = issue_acc(g - 1, pk, pj == 0, pj + 1 == pn, pt);
+    if (ok && pj >= 0) ok = issue_acc(g - 1, pk, pj == 0, pj + 1 == pn, pt, pfew);
     if (!ok && lane == 0) record_abort(abort_v, kSiteIssuer);
     mma_commit_elect(&drain);
     warp_wait(&drain, 0, abort_v, ok ? kTimeoutNs : kDrainTimeoutNs);
@@ -925,6 +942,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         ATTN_TR(20, j);  // S and dP of key tile j ready
         tc_fence_after();
         const uint32_t s_t = tmem + lane_off + BT * (g & 1) + BH2 * r;
+        if constexpr (FEW) {
+          if (wt.few && j == 0) {  // the sinks alone, by warpgroup 0
+            uint32_t sf[32], df[32];
+            if (r == 0) {
+              tmem_ld32_wait(s_t, sf);
+              tmem_ld32_wait(dp_t, df);
+            }
+            tc_fence_before();
+            mbar_arrive(&dp_free);
+            if (r == 0) {
+              const int n_vis = min(p.sinks, lim + 1);
+              uint32_t ds[32];
+#pragma unroll
+              for (int e = 0; e < 32; ++e) ds[e] = 0u;
+#pragma unroll
+              for (int e = 0; e < kFewKeys; e += 2) {
+                const float p0 = e < n_vis ? ex2_approx(fmaf(__uint_as_float(sf[e]), p.c, nl)) : 0.0f;
+                const float p1 = e + 1 < n_vis ? ex2_approx(fmaf(__uint_as_float(sf[e + 1]), p.c, nl)) : 0.0f;
+                const float y0 = e < n_vis ? p0 * (__uint_as_float(df[e]) + nd) : 0.0f;
+                const float y1 = e + 1 < n_vis ? p1 * (__uint_as_float(df[e + 1]) + nd) : 0.0f;
+                ds[e / 2] = pack_bf16x2(y0, y1);
+              }
+              tmem_st32(s_t, ds);
+              tmem_wait_st();
+              tc_fence_before();
+            }
+            mbar_arrive(&ds_full[r][g & 1]);
+            ATTN_TR(21, j);
+            continue;
+          }
+        }
         uint32_t sv[64], dpv[64];
         tmem_ld2x64_wait(s_t, dp_t, sv, dpv);
         tc_fence_before();
@@ -1041,11 +1089,13 @@ int prepare_device(int dev) {
                        reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<64, true>),
                        reinterpret_cast<const void*>(attn_bwd_dq_kernel<64, true>),
                        reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<128, true, true>),
-                       reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<64, true, true>)};
+                       reinterpret_cast<const void*>(attn_bwd_dkdv_kernel<64, true, true>),
+                       reinterpret_cast<const void*>(attn_bwd_dq_kernel<128, true, true>),
+                       reinterpret_cast<const void*>(attn_bwd_dq_kernel<64, true, true>)};
   const int bytes[] = {BCfg<128>::kSmemBytes, QCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes, QCfg<64>::kSmemBytes,
                        BCfg<128>::kSmemBytes, QCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes, QCfg<64>::kSmemBytes,
-                       BCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes};
-  for (int f = 0; f < 10 && e == cudaSuccess; ++f)
+                       BCfg<128>::kSmemBytes, BCfg<64>::kSmemBytes, QCfg<128>::kSmemBytes, QCfg<64>::kSmemBytes};
+  for (int f = 0; f < 12 && e == cudaSuccess; ++f)
     e = cudaFuncSetAttribute(fns[f], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[f]);
   if (e != cudaSuccess) return cuda_fail(e);
   if (!attn_host::encode_tiled_fn()) return ATTN_ERR_TENSOR_MAP;
@@ -1154,7 +1204,10 @@ int launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& 
   b.n_items = prm.n_qt * prm.BH;
   cfg.gridDim = dim3(b.n_items < sms ? b.n_items : sms);
   cfg.dynamicSmemBytes = QCfg<D>::kSmemBytes;
-  e = cudaLaunchKernelEx(&cfg, attn_bwd_dq_kernel<D, WINDOW>, tq, tk, tv, tdo, b);
+  if (WINDOW && prm.sinks > 0 && prm.sinks <= kFewKeys)
+    e = cudaLaunchKernelEx(&cfg, attn_bwd_dq_kernel<D, WINDOW, WINDOW>, tq, tk, tv, tdo, b);
+  else
+    e = cudaLaunchKernelEx(&cfg, attn_bwd_dq_kernel<D, WINDOW>, tq, tk, tv, tdo, b);
   if (WINDOW && e == cudaSuccess && (prm.head_groups > 1 || (prm.sink_tiles() > 0 && prm.sink_chunks > 1))) {
     const int64_t tiles = prm.head_groups > 1 ? prm.n_kt : prm.sink_tiles();
     const int64_t quads = tiles * prm.BZ * 2 * BT * (D / 4);
