@@ -160,7 +160,7 @@ struct Seq {
 __device__ __forceinline__ Seq seq_at(const Params& p, int b, bool& bad) {
   Seq s{0, 0, 0, 0};
   if (b >= p.rows) return s;
-  const int c0 = __ldg(p.cu + b), c1 = __ldg(p.cu + b + 1), len = __ldg(p.lens + b);
+  const int c0 = p.cu[b], c1 = p.cu[b + 1], len = p.lens[b];
   if (c0 < 0 || c1 < c0 || c1 > p.n_tokens) {
     bad = true;
     return s;
@@ -347,7 +347,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  griddep_launch_dependents();
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < KS; ++s) {
@@ -377,7 +376,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     abort_flag = 0;
     fence_mbar_init();
   }
-  // The planning warp's place in the list of key tiles, found while the others set up.
+  if (warp == kMmaWarp) {
+    tmem_alloc(&tmem_base_slot, kTmemCols);
+    tmem_relinquish();
+  }
+  // What is above overlaps the end of the kernel before this one in the stream (one token: 14.9 us in a
+  // stream of calls, 16.5 without).  That kernel may still write what is read below, so nothing is read through
+  // the read-only cache.
+  griddep_wait();
+  griddep_launch_dependents();
+  // The planning warp's place in the list of key tiles.
   int64_t per = 0, at = 0, end = 0;  // key tiles per CTA; this CTA's part of the list: [at, end)
   int b = 0, rt = 0, h = 0, s0 = 0;  // ... where it begins: sequence, item of it, kv head, step
   Seq seq{0, 0, 0, 0};
@@ -436,10 +444,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (rt * p.item_tokens >= seq.n || h >= p.Hkv) at = end;  // the lengths changed under the call
     }
   }
-  if (warp == kMmaWarp) {
-    tmem_alloc(&tmem_base_slot, kTmemCols);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -466,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t slots, uint32_t& n) -> bool {
     const int32_t* row = p.table + static_cast<int64_t>(item.b) * p.max_pages;
     const int used = (item.kv_len + p.page_size - 1) >> p.page_shift;
-    auto load_ids = [&](int w) { return w + lane < used ? __ldg(row + w + lane) : 0; };
+    auto load_ids = [&](int w) { return w + lane < used ? row[w + lane] : 0; };
     int win = -64, ids = 0, ids_next = 0;  // pages [win, win + 32) of the row, and the next 32 on their way
     for (int s = item.s0; s < item.s1; ++s, ++n) {
       const int key0 = item.tile(s) * BN;
@@ -876,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           int place = item.ctx + u;
           if (r.words) {
             place = item.ctx - 1;
-            for (int i = 0; i < n_words; ++i) place += __popc(__ldg(r.words + i) & range_bits(32 * i, 0, item.seq_n));
+            for (int i = 0; i < n_words; ++i) place += __popc(r.words[i] & range_bits(32 * i, 0, item.seq_n));
           }
           r.lo = place - p.window + 1;
         }
@@ -889,8 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (cur.words) {
           const int u0 = key - item.ctx;  // the drafted token of the word's first bit
           const int at = u0 >> 5;
-          const uint32_t a = at >= 0 && at < n_words ? __ldg(cur.words + at) : 0u;
-          const uint32_t z = at + 1 >= 0 && at + 1 < n_words ? __ldg(cur.words + at + 1) : 0u;
+          const uint32_t a = at >= 0 && at < n_words ? cur.words[at] : 0u;
+          const uint32_t z = at + 1 >= 0 && at + 1 < n_words ? cur.words[at + 1] : 0u;
           v |= __funnelshift_r(a, z, u0 & 31) & range_bits(u0, 0, item.seq_n);
         }
         return v;
@@ -1226,6 +1230,7 @@ template <int D>
 __global__ void __launch_bounds__(256) attn_tree_merge_kernel(const Params p) {
   constexpr int kVec = D / 32;
   griddep_wait();
+  griddep_launch_dependents();
   const int4 d = p.desc[blockIdx.x];  // tokens, first token, kv head, last CTA
   const int lane = threadIdx.x % 32;
   const int row = blockIdx.y * 8 + threadIdx.x / 32;  // of the two row tiles that an item may have
@@ -1357,23 +1362,30 @@ template <int D>
 int launch(const QMaps& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int sms,
            cudaStream_t stream) {
   const int grid = std::min(sms, kMaxCtas);
-  if (p.item_tokens > p.R)
-    attn_tree_kernel<D, true><<<grid, kThreads, Cfg<D, true>::kSmemBytes, stream>>>(tq, tk, tv, p);
-  else
-    attn_tree_kernel<D, false><<<grid, kThreads, Cfg<D, false>::kSmemBytes, stream>>>(tq, tk, tv, p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e);
+  // both kernels start under the one before them and wait for it with griddep_wait
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  if (p.item_tokens > p.R) {
+    cfg.dynamicSmemBytes = Cfg<D, true>::kSmemBytes;
+    e = cudaLaunchKernelEx(&cfg, attn_tree_kernel<D, true>, tq, tk, tv, p);
+  } else {
+    cfg.dynamicSmemBytes = Cfg<D, false>::kSmemBytes;
+    e = cudaLaunchKernelEx(&cfg, attn_tree_kernel<D, false>, tq, tk, tv, p);
+  }
+  if (e != cudaSuccess) return cuda_fail(e);
   // rows of an item: one row tile's, or all of the first's places and the second's
   const int rows = p.n_tokens <= p.R ? p.n_tokens * p.G : p.item_tokens == p.R ? p.R * p.G : BM + p.R * p.G;
   cfg.gridDim = dim3(grid, (rows + 7) / 8);
   cfg.blockDim = dim3(256);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   e = cudaLaunchKernelEx(&cfg, attn_tree_merge_kernel<D>, p);
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e);
 }
