@@ -170,7 +170,8 @@ __device__ __forceinline__ void record_abort(volatile uint32_t* abort_flag, int 
 // -D_i = -sum_d dO[i,d] O[i,d] (fp32, from the bf16 tensors) and -LSE_i * log2(e); rows
 // past Sq and rows without keys (LSE = -inf) get -inf, so their P is 0.  The values are
 // stored negated so the kernels add them with packed FMAs.
-template <int D>
+// AFTER (window mode, few blocks): starts under the kernel before it in the stream, the forward perhaps.
+template <int D, bool AFTER = false>
 __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const __nv_bfloat16* __restrict__ o,
                                                             const __nv_bfloat16* __restrict__ dout,
                                                             const float* __restrict__ lse, float* __restrict__ nlse2,
@@ -178,6 +179,11 @@ __global__ void __launch_bounds__(256) attn_bwd_prep_kernel(const __nv_bfloat16*
                                                             int Sq_pad) {
   constexpr int kLanesPerRow = D / 8;
   constexpr int kRowsPerWarp = 32 / kLanesPerRow;
+  if constexpr (AFTER) {
+    griddep_wait();
+    // nothing is read before that, nor through the read-only cache
+    asm volatile("" : "+l"(o), "+l"(dout), "+l"(lse)::"memory");
+  }
   const int lane = threadIdx.x % 32, sub = lane % kLanesPerRow;
   const int64_t row =
       (static_cast<int64_t>(blockIdx.x) * 8 + threadIdx.x / 32) * kRowsPerWarp + lane / kLanesPerRow;
@@ -617,6 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D>
 __global__ void __launch_bounds__(256) attn_bwd_parts_kernel(const BParams p) {
   griddep_wait();
+  griddep_launch_dependents();
   const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;  // [tile][z][dV, dK][key][D / 4]
   const int c4 = static_cast<int>(e % (D / 4));
   const int64_t row = e / (D / 4);  // (tile * BZ + z) * 2 * BT + (dV, dK) * BT + key
@@ -1177,21 +1184,32 @@ int launch_all(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& 
                float* lse2, float* delta, int sms, cudaStream_t stream) {
   const int64_t prep_rows = static_cast<int64_t>(prm.BH) * prm.Sq_pad;
   const int64_t prep_warps = (prep_rows + 32 / (D / 8) - 1) / (32 / (D / 8));
-  attn_bwd_prep_kernel<D><<<static_cast<unsigned>((prep_warps + 7) / 8), 256, 0, stream>>>(
-      o, dout, lse, lse2, delta, prm.BH, prm.Sq, prm.Sq_pad);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e);
   // the dK/dV and dQ kernels are launched with programmatic stream serialisation: each
   // may be scheduled before the previous kernel has finished (see griddep_* in ptx.cuh)
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = BCfg<D>::kSmemBytes;
+  cfg.gridDim = dim3(static_cast<unsigned>((prep_warps + 7) / 8));
+  cfg.blockDim = dim3(256);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // The window's prep kernel too, where its blocks fit the SMs at once (2 x 1000 tokens, 16 heads, D 64: 44.6 us
+  // in a stream of calls, 46.7 without).  With more, each block's own wait adds up: 16384 tokens, 32 heads, D
+  // 128: 1135 us for 1116.
+  cudaError_t e;
+  if (WINDOW && cfg.gridDim.x <= 8u * static_cast<unsigned>(sms)) {
+    e = cudaLaunchKernelEx(&cfg, attn_bwd_prep_kernel<D, WINDOW>, o, dout, lse, lse2, delta,
+                           static_cast<int64_t>(prm.BH), prm.Sq, prm.Sq_pad);
+  } else {
+    attn_bwd_prep_kernel<D><<<cfg.gridDim, cfg.blockDim, 0, stream>>>(o, dout, lse, lse2, delta, prm.BH, prm.Sq,
+                                                                      prm.Sq_pad);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return cuda_fail(e);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = BCfg<D>::kSmemBytes;
   BParams a = prm;
   a.n_items = static_cast<int>(kv_items);
   cfg.gridDim = dim3(a.n_items < sms ? a.n_items : sms);
