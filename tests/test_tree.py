@@ -17,7 +17,7 @@ import torch
 
 from attention_forward_06_gb300 import _lib, ops
 from attention_forward_06_gb300 import build as B
-from paged_model import i32, pool
+from paged_model import empty_cache, i32, pool
 from parity_util import compare
 from plain_attention import forward
 
@@ -393,6 +393,54 @@ def test_a_speculative_step_end_to_end():
     attend(append([1, 1, 5]))
     ops.kv_free(*cache[2:], i32([0, 1, 2]), P)
     assert not cache[4].any() and not cache[3].any()
+
+
+@gpu
+def test_calls_back_to_back_are_calls_one_by_one():
+    """Kernels of these calls start under the one before them: what the one before writes (lengths, tables, pages, the
+    tokens and offsets themselves) is read as it left it.  Every step's inputs come from kernels right before it."""
+    def run(wait):
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        cache = empty_cache(400, 4, 16, 128, 24, 40, seed=3)
+        g = torch.Generator(device="cuda").manual_seed(5)
+        new = lambda n, h: torch.randn((n, h, 128), generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+        ws = torch.empty(ops.tree_workspace_size(128), dtype=torch.uint8, device="cuda")
+        outs = []
+        one = torch.ones(25, dtype=torch.int32, device="cuda")
+
+        def step(each):  # every row gets `each` tokens and their attention
+            cu = (torch.cumsum(one, 0, dtype=torch.int32) - 1) * each
+            k, v, q = new(24 * each, 4), new(24 * each, 4), new(24 * each, 16)
+            pause()
+            outs.append(ops.kv_append(k, v, *cache, cu))
+            pause()
+            outs.extend(ops.attn_fwd_tree(q, *cache[:4], cu, workspace=ws))
+            pause()
+            return cu
+
+        for n in (37, 1, 1, 40, 1):
+            step(n)
+        cu = step(6)
+        acc = i32(np.tile([1, 4], 24))
+        outs.append(ops.kv_compact(*cache, cu, acc, (torch.cumsum(one, 0, dtype=torch.int32) - 1) * 2))
+        pause()
+        step(1)
+        for n in range(3):
+            kids = i32(np.arange(12, 24))
+            ops.kv_free(*cache[2:], kids, 16)
+            pause()
+            outs.append(ops.kv_fork(*cache, i32(np.arange(12)), kids))
+            pause()
+            step(1 + n)
+        torch.cuda.synchronize()
+        assert ops.paged_debug_status() == (ops.ATTN_OK, 0)
+        return outs + list(cache)
+
+    slow, fast = run(True), run(False)
+    assert not any(x.any() for x in slow if x.dtype == torch.int32 and x.numel() == 1)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(slow, fast))
+        fast = run(False)
 
 
 # ---------------------------------------------------------------------------- on the CPU

@@ -191,6 +191,34 @@ def test_in_a_graph_and_on_another_stream():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 8, 2, 500, 64, 100, 4), (2, 8, 8, 1000, 64, 200, 0), (1, 16, 1, 900, 128, 60, 20)],
+                         ids=IDS)
+def test_calls_back_to_back_are_calls_one_by_one(shape):
+    # a call starts under the kernel before it, which here writes what it reads: q, k, v and dO of each step come from
+    # kernels right before it, and the backward follows its forward at once
+    B, Hq, Hkv, S, D, window, sinks = shape
+
+    def run(wait):
+        pause = torch.cuda.synchronize if wait else (lambda: None)
+        base = [t.cuda() for t in draw(B, Hq, Hkv, S, S, D, seed=61)]
+        do = draw(B, Hq, Hkv, S, S, D, seed=62)[0].cuda()
+        outs = []
+        for step in range(6):
+            q, k, v, g = (t * (1.0 + 0.125 * step) for t in (*base, do))
+            pause()
+            o, lse = ops.attn_fwd_window(q, k, v, window, sinks=sinks)
+            pause()
+            outs += [o, lse, *ops.attn_bwd_window(q, k, v, o, lse, g, window, sinks=sinks)]
+            pause()
+        torch.cuda.synchronize()
+        return outs
+
+    slow = run(True)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(slow, run(False)))
+
+
+@pytest.mark.gpu
 def test_empty_sequences():
     q, k, v = [t.cuda() for t in draw(1, 2, 1, 64, 64, 128, seed=43)]
     o, lse = ops.attn_fwd_window(q, k[:, :, :0].contiguous(), v[:, :, :0].contiguous(), 4)
