@@ -243,7 +243,9 @@ size_t attn_fwd_tile_order_entries(int B, int order_heads, int Sq, int Sk);
  * other arguments, layouts and status codes as attn_fwd.  One kernel is enqueued
  * on `stream`; nothing is allocated.  The work order is heads fastest always
  * (consecutive query blocks share most of their window through L2), and
- * ATTN_FWD_ITEM_ORDER does not apply.  attn_bwd_window (attn_bwd.h) is its
+ * ATTN_FWD_ITEM_ORDER does not apply.  The kernel starts under the one before it in the
+ * stream and lets the next one start early: one of the caller's that is launched with
+ * programmatic stream serialisation has to wait for it (griddepcontrol.wait).  attn_bwd_window (attn_bwd.h) is its
  * backward; attn_fwd_tree (attn_paged.h) its form for single tokens over a cache.
  */
 int attn_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Sq,

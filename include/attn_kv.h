@@ -29,7 +29,9 @@
  * what the host knows (attn_fwd.h's status codes).  What only the device knows it
  * checks there: it then changes nothing and reports in `status` (device memory).
  * Calls on one cache must be ordered (one stream, or events); calls on different
- * caches may overlap.
+ * caches may overlap.  The kernels let the next one in the stream start early: a kernel
+ * of the caller's that is launched with programmatic stream serialisation has to wait for
+ * them (griddepcontrol.wait) before it touches what they read or write.
  */
 #ifndef ATTN_KV_H
 #define ATTN_KV_H

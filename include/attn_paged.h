@@ -42,7 +42,8 @@
  * in several ranges is merged by LSE in a second kernel, in a fixed order, so
  * results are the same from run to run.  Two kernels are enqueued on `stream`;
  * nothing is allocated and nothing waits for the device.  Calls that may run at the
- * same time need workspaces of their own.
+ * same time need workspaces of their own.  As in attn_kv.h, the kernels let the next one
+ * in the stream start early.
  */
 #ifndef ATTN_PAGED_H
 #define ATTN_PAGED_H
