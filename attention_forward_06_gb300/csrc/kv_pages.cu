@@ -360,14 +360,32 @@ __global__ void __launch_bounds__(256) kv_fork_move_kernel(const attn_kv_cache c
 // ---------------------------------------------------------------------------- compact
 // One block per row checks its lists and moves its tokens, then a second kernel gives pages
 // back and sets the lengths: a page counts as shared if it was before the call, whichever
-// block runs first.  Token i of the kept ones comes from place accepted[i] >= i, so moving them
+// block runs first.  Up to kTogether rows are a cluster, whose barrier stands for the second
+// kernel (0.7 us less on the GPU, 5 in a stream that the host paces).  Token i of the kept ones comes from place accepted[i] >= i, so moving them
 // in ascending order never overwrites a token that is still to move; a group of tokens is
 // read whole into registers before any of it is written.
 constexpr int kCompact = 512;  // threads
 constexpr int kHold = 4;       // 16-byte pieces of K and of V that a thread holds
 constexpr int kGroup = 128;    // tokens whose places are looked up at a time
+constexpr int kTogether = 8;   // blocks of a cluster
 
-template <int D>
+// One warp: the length of row b after its tokens have moved, and the pages past it.
+__device__ __forceinline__ void compact_end(const attn_kv_cache& c, const int32_t* cu, const int32_t* cu_accepted,
+                                            int b) {
+  const int lane = threadIdx.x % 32;
+  const int len = c.seq_lens[b];
+  const int end = len - (cu[b + 1] - cu[b]) + (cu_accepted[b + 1] - cu_accepted[b]);
+  int32_t* table = c.page_table + static_cast<int64_t>(b) * c.max_pages;
+  for (int p = pages_of(end, c.page_size) + lane; p < pages_of(len, c.page_size); p += 32) {
+    const int page = table[p];
+    if (page >= 0 && page < c.n_pages) atomicSub(&c.ref_counts[page], 1);
+    table[p] = -1;
+  }
+  __syncwarp();
+  if (lane == 0) c.seq_lens[b] = end;
+}
+
+template <int D, bool TOGETHER>
 __global__ void __launch_bounds__(kCompact) kv_compact_kernel(const attn_kv_cache c, const int32_t* cu,
                                                               const int32_t* accepted, int n_accepted,
                                                               const int32_t* cu_accepted,
@@ -401,6 +419,8 @@ __global__ void __launch_bounds__(kCompact) kv_compact_kernel(const attn_kv_cach
   }
   bad = __syncthreads_or(bad);
   if (tid == 0) status[b] = bad ? ATTN_KV_INVALID : 0;
+  if constexpr (TOGETHER)  // every row has looked at the counts
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
   if (bad) return;
   // ---- move
   const int per = c.Hkv * kChunks;           // 16-byte pieces of one token's K (and of its V)
@@ -444,26 +464,19 @@ __global__ void __launch_bounds__(kCompact) kv_compact_kernel(const attn_kv_cach
       __syncthreads();  // ... and written before the next one is read
     }
   }
+  if constexpr (TOGETHER) {
+    __syncthreads();  // the length and the table have been read
+    if (tid < 32) compact_end(c, cu, cu_accepted, b);
+  }
 }
 
-// The lengths after kv_compact_kernel, and the pages past them, a warp per row.
+// After kv_compact_kernel, a warp per row.
 __global__ void __launch_bounds__(256) kv_compact_end_kernel(const attn_kv_cache c, const int32_t* cu,
-                                                             const int32_t* cu_accepted,
-                                                             const int32_t* status) {
-  const int b = blockIdx.x * 8 + threadIdx.x / 32, lane = threadIdx.x % 32;
+                                                             const int32_t* cu_accepted, const int32_t* status) {
+  const int b = blockIdx.x * 8 + threadIdx.x / 32;
   griddep_wait();
   griddep_launch_dependents();
-  if (b >= c.rows || status[b] != 0) return;
-  const int len = c.seq_lens[b];
-  const int end = len - (cu[b + 1] - cu[b]) + (cu_accepted[b + 1] - cu_accepted[b]);
-  int32_t* table = c.page_table + static_cast<int64_t>(b) * c.max_pages;
-  for (int p = pages_of(end, c.page_size) + lane; p < pages_of(len, c.page_size); p += 32) {
-    const int page = table[p];
-    if (page >= 0 && page < c.n_pages) atomicSub(&c.ref_counts[page], 1);
-    table[p] = -1;
-  }
-  __syncwarp();
-  if (lane == 0) c.seq_lens[b] = end;
+  if (b < c.rows && status[b] == 0) compact_end(c, cu, cu_accepted, b);
 }
 
 // ---------------------------------------------------------------------------- free
@@ -520,6 +533,24 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
+// As launch_after, the blocks one cluster.
+template <class... P, class... A>
+cudaError_t launch_cluster(void (*kernel)(P...), int blocks, int threads, cudaStream_t stream, A... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(blocks);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 
@@ -623,7 +654,11 @@ int attn_kv_compact(const attn_kv_cache* cache, const int32_t* cu_tokens, const 
   int sms = 0;
   st = device(&sms);
   if (st != ATTN_OK) return st;
-  const cudaError_t e = launch_after(cache->D == 128 ? kv_compact_kernel<128> : kv_compact_kernel<64>,
+  if (cache->rows <= kTogether)
+    return done(launch_cluster(cache->D == 128 ? kv_compact_kernel<128, true> : kv_compact_kernel<64, true>,
+                               cache->rows, kCompact, stream, *cache, cu_tokens, accepted, n_accepted, cu_accepted,
+                               status));
+  const cudaError_t e = launch_after(cache->D == 128 ? kv_compact_kernel<128, false> : kv_compact_kernel<64, false>,
                                      dim3(cache->rows), kCompact, 0, stream, *cache, cu_tokens, accepted, n_accepted,
                                      cu_accepted, status);
   if (e != cudaSuccess) return cuda_fail(e);
