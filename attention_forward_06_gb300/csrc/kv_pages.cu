@@ -361,9 +361,10 @@ __global__ void __launch_bounds__(256) kv_fork_move_kernel(const attn_kv_cache c
 // One block per row checks its lists and moves its tokens, then a second kernel gives pages
 // back and sets the lengths: a page counts as shared if it was before the call, whichever
 // block runs first.  Up to kTogether rows are a cluster, whose barrier stands for the second
-// kernel (0.7 us less on the GPU, 5 in a stream that the host paces).  Token i of the kept ones comes from place accepted[i] >= i, so moving them
-// in ascending order never overwrites a token that is still to move; a group of tokens is
-// read whole into registers before any of it is written.
+// kernel (0.7 us less on the GPU, 5 in a stream that the host paces).  Token i of the kept
+// ones comes from place accepted[i] >= i, so moving them in ascending order never
+// overwrites a token that is still to move; a group of tokens is read whole into registers
+// before any of it is written.
 constexpr int kCompact = 512;  // threads
 constexpr int kHold = 4;       // 16-byte pieces of K and of V that a thread holds
 constexpr int kGroup = 128;    // tokens whose places are looked up at a time
@@ -612,9 +613,8 @@ int attn_kv_append(const attn_kv_cache* cache, const void* k_new, const void* v_
   const NewTokens x{static_cast<const __nv_bfloat16*>(k_new), static_cast<const __nv_bfloat16*>(v_new),
                     k_stride_token, k_stride_head, v_stride_token, v_stride_head};
   const int blocks = std::min(n_tokens / 8 + 1, sms * 8);
-  return done(cache->D == 128
-                  ? launch_after(kv_append_write_kernel<128>, dim3(blocks), 256, 0, stream, *cache, x, cu_tokens, status)
-                  : launch_after(kv_append_write_kernel<64>, dim3(blocks), 256, 0, stream, *cache, x, cu_tokens, status));
+  return done(launch_after(cache->D == 128 ? kv_append_write_kernel<128> : kv_append_write_kernel<64>, dim3(blocks),
+                           256, 0, stream, *cache, x, cu_tokens, status));
 }
 
 int attn_kv_fork(const attn_kv_cache* cache, const int32_t* parents, const int32_t* children, int n, int32_t* status,
@@ -636,9 +636,8 @@ int attn_kv_fork(const attn_kv_cache* cache, const int32_t* parents, const int32
   if (e != cudaSuccess) return cuda_fail(e);
   if (n == 0) return ATTN_OK;
   const dim3 grid(n, 1 + cache->Hkv);
-  return done(cache->D == 128
-                  ? launch_after(kv_fork_move_kernel<128>, grid, 256, 0, stream, *cache, parents, children, status)
-                  : launch_after(kv_fork_move_kernel<64>, grid, 256, 0, stream, *cache, parents, children, status));
+  return done(launch_after(cache->D == 128 ? kv_fork_move_kernel<128> : kv_fork_move_kernel<64>, grid, 256, 0, stream,
+                           *cache, parents, children, status));
 }
 
 int attn_kv_compact(const attn_kv_cache* cache, const int32_t* cu_tokens, const int32_t* accepted, int n_accepted,
